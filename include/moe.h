@@ -206,6 +206,26 @@ moe_status moe_forward(const moe_dims* d, const void* x, const void* w_router, c
                        const void* residual, void* out, int32_t* topk_idx, float* topk_w,
                        void* ws, size_t ws_bytes, void* stream);
 
+/* The whole layer for a few tokens (0 <= T <= 16) in two launches: the same
+ * layer, arguments and workspace as moe_forward, for the decode steps of a few
+ * requests, where moe_forward's launches and its tiles of 64 token rows cost
+ * more than the few expert rows they serve.
+ *  - expert_dtype MOE_BF16 (with or without a shared expert), MOE_FP8_E4M3 or
+ *    MOE_FP8_B128; T > 16 and MOE_NVFP4 return MOE_EUNSUPPORTED.
+ *  - Indices are those of moe_route bit for bit, weights within fp32 rounding.
+ *  - out differs from moe_forward's in rounding only: the expert outputs are not
+ *    rounded to bf16 before the weighted sum, which runs in fp32 in ascending
+ *    expert order (then the shared chunks, then the residual), and bf16 experts
+ *    keep 16 bits of the ReLU^2 tensor instead of 8.  E4M3 experts divide it by
+ *    h_scale (correctly rounded) before the code.  A token's bits do not depend on
+ *    which other tokens share its batch.
+ *  - out may alias residual, but not x.  Calls that may overlap on the GPU need
+ *    workspaces of their own, as with moe_forward. */
+moe_status moe_forward_few(const moe_dims* d, const void* x, const void* w_router, const float* bias,
+                           const void* w_up, const void* w_down, const void* w_up_shared,
+                           const void* w_down_shared, const moe_fp8_scales* scales, const void* residual,
+                           void* out, int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes, void* stream);
+
 /* Row gather: out[r] = x[perm_src[r] / K] for r < rows, rows of H bf16 values
  * (16-byte aligned).  This is the step moe_expert_ffn applies to the token
  * rows before the up projection, exposed for callers that move rows between
@@ -291,6 +311,45 @@ moe_status moe_quantize_act_nvfp4(int64_t rows, int32_t H, float x_scale, const 
  *   x, u [T][H] bf16 (u may not alias x).  Cited: audio.cpp model page,
  * "Q4_K, Q3_K and Q2_K expert profiles" (the model's normalisation). */
 moe_status moe_rmsnorm(int64_t T, int32_t H, float eps, const void* x, void* u, void* stream);
+
+/* The norm before a block, with its gain, as bf16 and / or FP8_B128 codes:
+ *   v[t] = x[t] / sqrt(mean(x[t]^2) + eps) * gain
+ *   u[t] = bf16(v[t])
+ *   scales[t][b] = max|v[t]| over the 128 values of block b / 448 (1 for an all-zero block)
+ *   codes[t][h] = e4m3(fl32(v[t][h] / scales[t][h / 128])), nearest-even, saturating; zero past H
+ * All sums and v in fp32 (the codes come from v before its rounding to bf16).
+ *   x, u [T][H] bf16; gain [H] bf16 or NULL (1); codes [T][Kp(H)], scales [T][Kp(H)/128]
+ *   fp32, Kp(H) = 128*ceil(H/128): both given or both NULL; u may be NULL when codes are given.
+ * u may alias x.  16 <= H <= 65536, a multiple of 16; T < 2^31.  Cited: audio.cpp
+ * model page, "Q4_K, Q3_K and Q2_K expert profiles" (the model's normalisation);
+ * bloomery page s.3 (FP8_B128). */
+moe_status moe_prenorm(int64_t T, int32_t H, float eps, const void* x, const void* gain, void* u, uint8_t* codes,
+                       float* scales, void* stream);
+
+/* The norm after a block with its gate and residual scale, the residual sum and
+ * the norm before the next block, in one pass:
+ *   x'[t] = x[t] + alpha * gate * (y[t] / sqrt(mean(y[t]^2) + eps) * gain)
+ *   x_out[t] = bf16(x'[t])
+ *   u, codes, scales: moe_prenorm of x' (fp32, before its rounding) with next_gain and eps;
+ *   all three NULL: x_out only.
+ *   y, x, x_out [T][H] bf16; gain, next_gain [H] bf16 or NULL (1); gate bf16 or NULL (1):
+ *   [H] with gate_ld 0, or [T][H] with gate_ld H.  x_out may alias x or y, u may alias y;
+ *   x_out and u are different.  Sizes as in moe_prenorm. */
+moe_status moe_postnorm(int64_t T, int32_t H, float eps, float alpha, const void* y, const void* gain,
+                        const void* gate, int64_t gate_ld, const void* x, void* x_out, const void* next_gain,
+                        void* u, uint8_t* codes, float* scales, void* stream);
+
+/* Dense product of FP8_B128 operands (E4M3 codes with one fp32 scale per 128
+ * values along K of each row, the layout moe_quantize_fp8_b128 and the norms write):
+ *   z[m][n] = sum_b x_scales[m][b] * w_scales[n][b] * sum_{k in block b} x[m][k] * w[n][k]
+ *   out[m][n] = bf16(z) (MOE_ACT_NONE) or bf16(relu(z)^2) (MOE_ACT_RELU2), summed in fp32.
+ *   x_codes [M][Kp(K)], x_scales [M][Kp(K)/128], w_codes [N][Kp(K)], w_scales
+ *   [N][Kp(K)/128], out [M][N] bf16; codes past K zero in both operands.
+ * 0 <= M < 2^31 - 128; 16 <= N <= 2^20, 16 <= K <= 65536, both multiples of 16.  No workspace.
+ * Cited: bloomery page s.3 ("Kernel dispatch": FP8_B128), s.2 (ReLU^2). */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU2 = 1 } moe_act;
+moe_status moe_linear_fp8_b128(int64_t M, int32_t N, int32_t K, const uint8_t* x_codes, const float* x_scales,
+                               const uint8_t* w_codes, const float* w_scales, int32_t act, void* out, void* stream);
 
 /* The router (as moe_route) without a caller-provided workspace.  The paper
  * has no counterpart: this entry point serves callers that cannot allocate

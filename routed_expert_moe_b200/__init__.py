@@ -54,6 +54,13 @@ _SIG = {
     "moe_combine": (ctypes.c_int, [_DIMS, _P, _P, _P, _P, _P, _P]),
     "moe_forward": (ctypes.c_int, [_DIMS, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(MoeFp8Scales), _P, _P,
                                    _P, _P, _P, _S, _P]),
+    "moe_forward_few": (ctypes.c_int, [_DIMS, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(MoeFp8Scales), _P, _P,
+                                       _P, _P, _P, _S, _P]),
+    "moe_prenorm": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32, ctypes.c_float, _P, _P, _P, _P, _P, _P]),
+    "moe_postnorm": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_float, _P, _P, _P,
+                                    ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_linear_fp8_b128": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P,
+                                           ctypes.c_int32, _P, _P]),
     "moe_gather_rows": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P, _P,
                                        _P, _P]),
     "moe_ep_regroup": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, _P, _P, _P, _P, _P]),
@@ -214,6 +221,19 @@ def forward(d, x, w_router, bias, w_up, w_down, out, ws, scales=None, residual=N
                             _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "moe_forward")
 
 
+FEW_MAX_TOKENS = 16
+
+
+def forward_few(d, x, w_router, bias, w_up, w_down, out, ws, scales=None, residual=None, topk_idx=None,
+                topk_w=None, stream=None, shared=None):
+    """The whole layer for at most FEW_MAX_TOKENS tokens in two launches; arguments as forward()."""
+    sp = ctypes.byref(scales) if scales is not None else None
+    su, sd = shared if shared is not None else (None, None)
+    _check(_lib.moe_forward_few(ctypes.byref(d), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(w_up), _ptr(w_down),
+                                _ptr(su), _ptr(sd), sp, _ptr(residual), _ptr(out), _ptr(topk_idx), _ptr(topk_w),
+                                _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "moe_forward_few")
+
+
 def gather_rows(x, perm_src, out, K=1, stream=None):
     """out[r] = x[perm_src[r] // K] for the rows of out (bf16 rows of x [src_rows, H])."""
     rows, H = out.shape[0], x.shape[1]
@@ -254,6 +274,69 @@ def quantize_act_nvfp4(x, codes, block, x_scale, stream=None):
 def rmsnorm(x, u, eps=1e-5, stream=None):
     T, H = x.shape
     _check(_lib.moe_rmsnorm(T, H, float(eps), _ptr(x), _ptr(u), _stream(stream)), "moe_rmsnorm")
+
+
+def _arg(t, where, dtype, *shape):
+    """Pointer of a dense tensor of this type and shape on the current device (None passes through)."""
+    import torch
+    if t is None:
+        return None
+    if (t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous()
+            or t.get_device() != torch.cuda.current_device()):
+        raise MoeError(MOE_EINVAL, f"{where}: needs a contiguous {dtype} tensor of shape {shape} on the current "
+                                   f"CUDA device, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _codes(codes, scales, where, rows, K):
+    import torch
+    kp = b128_kp(K)
+    return (_arg(codes, where, torch.uint8, rows, kp), _arg(scales, where, torch.float32, rows, kp // 128))
+
+
+def prenorm(x, gain=None, u=None, codes=None, scales=None, eps=1e-5, stream=None):
+    """The norm before a block: x [T, H] bf16 / rms * gain into u [T, H] (bf16) and / or FP8_B128 codes
+    [T, b128_kp(H)] with scales [T, b128_kp(H) / 128]."""
+    import torch
+    bf, w = torch.bfloat16, "moe_prenorm"
+    T, H = x.shape
+    c, s = _codes(codes, scales, w, T, H)
+    _check(_lib.moe_prenorm(T, H, eps, _arg(x, w, bf, T, H), _arg(gain, w, bf, H), _arg(u, w, bf, T, H), c, s,
+                            _stream(stream)), w)
+
+
+def postnorm(y, gain, x, x_out, gate=None, alpha=1.0, eps=1e-5, next_gain=None, u=None, codes=None, scales=None,
+             stream=None):
+    """x_out = x + alpha * gate * (y / rms(y) * gain); then prenorm of that sum with next_gain into u and / or
+    codes, scales (none of them: x_out only).  gate: [H] or [T, H] or None."""
+    import torch
+    bf, w = torch.bfloat16, "moe_postnorm"
+    T, H = x.shape
+    c, s = _codes(codes, scales, w, T, H)
+    per_token = gate is not None and gate.dim() == 2
+    g = _arg(gate, w, bf, T, H) if per_token else _arg(gate, w, bf, H)
+    _check(_lib.moe_postnorm(T, H, eps, alpha, _arg(y, w, bf, T, H), _arg(gain, w, bf, H), g, H if per_token else 0,
+                             _arg(x, w, bf, T, H), _arg(x_out, w, bf, T, H), _arg(next_gain, w, bf, H),
+                             _arg(u, w, bf, T, H), c, s, _stream(stream)), w)
+
+
+MOE_ACT_NONE, MOE_ACT_RELU2 = 0, 1
+_ACTS = {None: MOE_ACT_NONE, "none": MOE_ACT_NONE, "relu2": MOE_ACT_RELU2}
+
+
+def linear_fp8_b128(x_codes, x_scales, w_codes, w_scales, out, act=None, stream=None):
+    """out [M, N] (bf16) = act(x w^T) of FP8_B128 operands: codes [rows, Kp] (uint8, Kp a multiple of 128), scales
+    [rows, Kp / 128] (fp32); act: None or "relu2"."""
+    import torch
+    w = "moe_linear_fp8_b128"
+    M, Kp = x_codes.shape
+    N = w_codes.shape[0]
+    if act not in _ACTS or Kp % 128:
+        raise MoeError(MOE_EINVAL, f"{w}: act {act!r}, code rows of {Kp} bytes")
+    xc, xs = _codes(x_codes, x_scales, w, M, Kp)
+    wc, ws = _codes(w_codes, w_scales, w, N, Kp)
+    _check(_lib.moe_linear_fp8_b128(M, N, Kp, xc, xs, wc, ws, _ACTS[act], _arg(out, w, torch.bfloat16, M, N),
+                                    _stream(stream)), w)
 
 
 def check_device_error(stream=None):

@@ -223,6 +223,25 @@ ForwardWs carve_forward(Carve& c, void* base, const moe_dims* d) {
     return f;
 }
 
+FewWs carve_few(Carve& c, void* base, const moe_dims* d) {
+    FewWs f;
+    const bool fp8 = d->expert_dtype != MOE_BF16;
+    f.counters = c.take<int>(base, 2);
+    f.logits = c.take<long long>(base, (size_t)d->T * d->E);
+    f.xq = fp8 ? c.take<uint8_t>(base, (size_t)d->T * d->H) : nullptr;
+    f.h = c.take<uint8_t>(base, (size_t)ffn_rows(d) * d->F * (fp8 ? 1 : 4));
+    return f;
+}
+
+// Whether moe_forward_few takes these (valid) dims.
+bool few_supported(const moe_dims* d) { return d->T <= kFewMaxTokens && d->expert_dtype != MOE_NVFP4; }
+
+size_t few_ws_bytes(const moe_dims* d) {
+    Carve c;
+    carve_few(c, nullptr, d);
+    return c.off;
+}
+
 size_t route_ws_bytes(const moe_dims* d, int sms) {
     Carve c;
     carve_route(c, nullptr, d, router_plan(d->T, d->H, d->E, sms));
@@ -416,6 +435,7 @@ moe_status moe_workspace_size(const moe_dims* d, size_t* bytes) {
     // plans depend on the SM count only through the router split; size for
     // the largest split any device can choose
     *bytes = forward_ws_bytes(d, 1024);
+    if (few_supported(d)) *bytes = std::max(*bytes, few_ws_bytes(d));
     return MOE_OK;
 }
 
@@ -564,6 +584,34 @@ moe_status moe_forward(const moe_dims* d, const void* x, const void* w_router, c
                        n_shared(d), d->H, dev->num_sms, ctx, st);
     stage_mark(7, st);
     return cuda_status(e);
+}
+
+moe_status moe_forward_few(const moe_dims* d, const void* x, const void* w_router, const float* bias,
+                           const void* w_up, const void* w_down, const void* w_up_shared, const void* w_down_shared,
+                           const moe_fp8_scales* scales, const void* residual, void* out, int32_t* topk_idx,
+                           float* topk_w, void* ws, size_t ws_bytes, void* stream) {
+    moe_status s = check_dims(d);
+    if (s != MOE_OK) return s;
+    if (!few_supported(d)) return MOE_EUNSUPPORTED;
+    if ((s = check_fp8_scales(d, scales)) != MOE_OK) return s;
+    if ((s = check_shared(d, w_up_shared, w_down_shared)) != MOE_OK) return s;
+    if (d->T > 0 && (!x || !w_router || !w_up || !w_down || !out || !ws)) return MOE_EINVAL;
+    if (!aligned(x, 16) || !aligned(w_router, 16) || !aligned(w_up, 16) || !aligned(w_down, 16) ||
+        !aligned(residual, 16) || !aligned(out, 16) || !aligned(ws, 256) || !aligned(bias, 4) ||
+        !aligned(topk_idx, 4) || !aligned(topk_w, 4))
+        return MOE_EINVAL;
+    if (d->T > 0 && out == x) return MOE_EINVAL;
+    if (d->T == 0) return MOE_OK;
+    DeviceInfo* dev = nullptr;
+    if ((s = device_setup(&dev)) != MOE_OK) return s;
+    Carve c;
+    const FewWs fw = carve_few(c, ws, d);
+    if (c.off > ws_bytes) return MOE_EWORKSPACE;
+    return cuda_status(launch_few(d, static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w_router), bias,
+                                  w_up, w_down, w_up_shared, w_down_shared, scales,
+                                  static_cast<const uint16_t*>(residual), static_cast<uint16_t*>(out), topk_idx,
+                                  topk_w, fw, g_debug_withhold.load(), dev->num_sms, make_ctx(dev),
+                                  static_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_gather_rows(int64_t rows, int64_t src_rows, int32_t H, int32_t K, const void* x,

@@ -627,7 +627,7 @@ static EncodeTiledFnB encode_fn_b128() {
 }
 
 // 2-D map over a row-major u8 [rows][cols] matrix, box 128 bytes x box_rows, 128-byte swizzle.
-static bool make_map_u8_b128(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows) {
+bool make_map_u8_b128(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows) {
     EncodeTiledFnB fn = encode_fn_b128();
     if (!fn) return false;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};

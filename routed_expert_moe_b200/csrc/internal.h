@@ -97,6 +97,8 @@ cudaError_t launch_grouped_ffn_b128(const uint8_t* w_up, const float* su, const 
                                     const int4* sched, const int* n_sched, int bn, int max_sched, int* done,
                                     float x_scale, float h_scale, int num_sms, int debug_hold, const DevCtx& ctx,
                                     cudaStream_t stream);
+// 2-D map over a row-major u8 [rows][cols] matrix, box 128 bytes x box_rows, 128-byte swizzle.
+bool make_map_u8_b128(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows);
 cudaError_t launch_quantize_fp8_b128(int64_t rows, int K, const uint16_t* src, uint8_t* codes, float* scales,
                                      int num_sms, cudaStream_t stream);
 cudaError_t launch_combine(const uint16_t* yp, const int32_t* inv_row, const float* w, const uint16_t* residual,
@@ -110,6 +112,20 @@ cudaError_t launch_quantize(int64_t n_tensors, int64_t elems, const uint16_t* sr
 
 cudaError_t launch_ep_regroup(const int64_t* recv_counts, int W, int E_loc, int64_t R, int32_t* offsets,
                               int32_t* perm, int32_t* inv, const DevCtx& ctx, cudaStream_t stream);
+
+// The few-token layer (few.cu): at most this many tokens, two columns' worth of the 8-column
+// matrix instruction.
+constexpr int kFewMaxTokens = 16;
+struct FewWs {
+    int* counters;        // [2]: unit claims, up reports
+    long long* logits;    // [T][E]
+    uint8_t* xq;          // E4M3 codes of x [T][H] (quantised experts)
+    uint8_t* h;           // ReLU^2 rows [T*(K+ns)][F]: E4M3 codes, or bf16 high parts and then low parts
+};
+cudaError_t launch_few(const moe_dims* d, const uint16_t* x, const uint16_t* wr, const float* bias, const void* w_up,
+                       const void* w_down, const void* w_up_s, const void* w_down_s, const moe_fp8_scales* sc,
+                       const uint16_t* residual, uint16_t* out, int32_t* idx, float* w, const FewWs& ws, int hold,
+                       int num_sms, const DevCtx& ctx, cudaStream_t stream);
 
 // Token rows per schedule entry of the FP8_B128 grouped GEMM: its epilogue
 // keeps one running fp32 sum per row in registers.

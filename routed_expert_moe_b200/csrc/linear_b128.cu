@@ -1,0 +1,534 @@
+// Dense product of FP8_B128 operands (bloomery issue page, s.3 "Kernel
+// dispatch": the FP8 release's block-scaled matrices; s.2: ReLU^2):
+//
+//   z[m,n]   = sum_b sx[m,b] * sw[n,b] * sum_{k in block b} qx[m,k] qw[n,k]
+//   out[m,n] = bf16(z) or bf16(relu(z)^2)
+//
+// E4M3 codes, one fp32 scale per 128 values along K of each row of either
+// operand, fp32 sums.  Two kernels by the number of rows M:
+//
+//  - M <= 16: a weight stream.  Every CTA owns an equal share of the N weight
+//    rows over the whole of K (few.cuh: bulk-copy ring, warp-level products,
+//    eight warps split K and add their sums once).  Bound: HBM bytes.
+//  - above: tcgen05 tiles of 128 rows of x by BN rows of w.  A 128-byte K
+//    stage is one scale block, so its product goes to a TMEM slot of its own
+//    and eight epilogue warps, which hold the tile's fp32 sums in registers,
+//    add it times both scales while the tensor core fills the next slot.
+#include <algorithm>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+
+#include "few.cuh"
+
+namespace moe {
+
+struct LinearArgs {
+    const uint8_t* xq;    // [M][Kp]
+    const float* xs;      // [M][kb]
+    const uint8_t* wq;    // [N][Kp]
+    const float* ws;      // [N][kb]
+    uint16_t* out;        // [M][N]
+    int64_t M;
+    int N, Kp, kb;
+    int relu2;
+};
+
+__device__ __forceinline__ float lin_act(float z, int relu2) {
+    return relu2 ? (z <= 0.0f ? 0.0f : __fmul_rn(z, z)) : z;   // a NaN stays one
+}
+
+// ----------------------------------------------------------------------------- few rows
+
+struct LinearFewArgs {
+    LinearArgs l;
+    FwCut cut;
+    FwShare share;
+    int stride, slot_bytes, n_stages;
+};
+
+template <int NT>
+__global__ void __launch_bounds__(FW_THREADS, 1) linear_few_kernel(LinearFewArgs a, DevCtx ctx) {
+    extern __shared__ __align__(1024) uint8_t lf_smem[];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    FwRed<NT> red;
+    red.buf = reinterpret_cast<float*>(lf_smem + (size_t)FW_WARPS * a.n_stages * a.slot_bytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(red.buf + 2 * FwRed<NT>::kFloats);
+    uint64_t* rbar = bars + FW_WARPS * FW_MAX_STAGES;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(rbar + 1);
+    red.bar = smem_u32(rbar);
+    red.turn = 0;
+    FwRing ring;
+    ring.base = smem_u32(lf_smem) + warp * a.n_stages * a.slot_bytes;
+    ring.bars = smem_u32(bars + warp * FW_MAX_STAGES);
+    ring.slot_bytes = a.slot_bytes;
+    ring.stride = a.stride;
+    ring.n = a.n_stages;
+    ring.put = ring.take = 0;
+    ring.parity = 0;
+    ring.policy = l2_policy_evict_first();
+    if (lane == 0)
+        for (int s = 0; s < a.n_stages; ++s) mbar_init(ring.bars + 8 * s, 1);
+    if (tid == 0) {
+        mbar_init(smem_u32(rbar), FW_WARPS);
+        *abort_flag = 0;
+    }
+    if (lane == 0) fence_mbar_init();
+    __syncthreads();
+    pdl_enter();
+
+    const LinearArgs& l = a.l;
+    const int n_groups = gridDim.x * a.share.units * a.share.groups;
+    const int my_group = warp * a.share.groups / FW_WARPS, gw = FW_WARPS / a.share.groups, wk = warp % gw;
+    auto group_row = [&](int u, int grp) { return (int)((int64_t)(u * a.share.groups + grp) * l.N / n_groups); };
+    int f_unit = -1, f_k = 0, f_n0 = 0, f_n = 0;   // the next stage to fill: chunks wk, wk + gw, .. of each unit
+    auto next_unit = [&]() {
+        ++f_unit;
+        f_k = wk;
+        const int u = blockIdx.x * a.share.units + f_unit;
+        f_n0 = group_row(u, my_group);
+        f_n = group_row(u, my_group + 1) - f_n0;
+    };
+    next_unit();
+    auto fill_next = [&]() {
+        while (f_unit < a.share.units) {
+            if (f_k < a.cut.n && f_n > 0) {
+                ring.fill(l.wq + (int64_t)f_n0 * l.Kp + f_k * a.cut.chunk, l.Kp, f_n,
+                          (uint32_t)min(a.cut.chunk, l.Kp - f_k * a.cut.chunk));
+                f_k += gw;
+                return;
+            }
+            next_unit();
+        }
+    };
+    for (int s = 0; s < a.n_stages; ++s) fill_next();
+
+    const int g = lane / 4, q = lane % 4;
+    const int M = (int)l.M;
+    FwRows<NT> act;
+    const float* xs[NT][2];   // scale rows of this lane's result columns
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        act.on[nt] = nt * 8 + g < M;
+        act.p[nt] = l.xq + (int64_t)(nt * 8 + g) * l.Kp + q * 16;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) xs[nt][c] = nt * 8 + 2 * q + c < M ? l.xs + (int64_t)(nt * 8 + 2 * q + c) * l.kb : nullptr;
+    }
+    for (int un = 0; un < a.share.units; ++un) {
+        const int u = blockIdx.x * a.share.units + un;
+        const int n0 = group_row(u, my_group), n = group_row(u, my_group + 1) - n0;
+        const float* ws0 = l.ws + (int64_t)(n0 + min(g, max(n, 1) - 1)) * l.kb;
+        const float* ws1 = l.ws + (int64_t)(n0 + min(g + 8, max(n, 1) - 1)) * l.kb;
+        float acc[NT][4] = {};
+        for (int k = wk; k < a.cut.n && n > 0; k += gw) {
+            const int c0 = k * a.cut.chunk, bytes = min(a.cut.chunk, l.Kp - c0);
+            auto load = [&](auto& v, int seg0, int n_seg) {
+                const int off = c0 + seg0 * FW_SEG;
+                fw_load(v, act, off, n_seg, l.Kp, 0);
+#pragma unroll
+                for (int s = 0; s < FW_GROUP / 2; ++s)
+                    if (2 * s < n_seg) {
+                        v.ws[s][0] = __ldg(ws0 + off / 128 + s);
+                        v.ws[s][1] = __ldg(ws1 + off / 128 + s);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                v.xs[s][nt][c] = xs[nt][c] ? __ldg(xs[nt][c] + off / 128 + s) : 0.0f;
+                    }
+            };
+            if (!fw_stage<false, NT, false, true, true>(acc, ring, n, bytes, load, ctx, abort_flag)) return fw_settle();
+            fill_next();
+        }
+        if (!red.exchange(acc, warp, ctx, abort_flag)) return fw_settle();
+        const int r0 = group_row(u, 0), rows = group_row(u, a.share.groups) - r0;
+        const int half = group_row(u, 1) - r0;   // rows of the first group
+        for (int j = tid; j < rows * M; j += FW_THREADS) {
+            const int t = j / rows, row = j - t * rows;
+            const float z = row < half ? red.sum(row, t, 0, gw) : red.sum(row - half, t, gw, gw);
+            l.out[(int64_t)t * l.N + r0 + row] = __bfloat16_as_ushort(__float2bfloat16_rn(lin_act(z, l.relu2)));
+        }
+    }
+}
+
+// ----------------------------------------------------------------------------- tiles
+
+constexpr int LT_BM = 128;              // rows of x per tile (TMEM lanes)
+constexpr int LT_KB = 128;              // bytes of K per stage: one scale block
+constexpr int LT_EPI = 8;               // epilogue warps: two per TMEM lane quadrant
+constexpr int LT_THREADS = 32 * (2 + LT_EPI);
+constexpr int LT_SS = 8;                // slots of the scale ring
+constexpr int LT_MAX_STAGES = 8;
+
+template <int BN>
+struct LtShape {
+    static constexpr int kSlots = BN >= 256 ? 2 : 4;                  // TMEM partial products
+    static constexpr int kTmem = kSlots * BN;                          // columns
+    static constexpr int kStage = (LT_BM + BN) * LT_KB;
+    static constexpr int kScale = (LT_BM + BN) * 4;                    // bytes of a scale slot
+    static constexpr int kCols = BN / 2;                               // columns of an epilogue warp
+};
+
+struct LinearTileArgs {
+    LinearArgs l;
+    int m_tiles, n_tiles;
+    int n_stages;
+};
+
+struct LinearMaps {
+    CUtensorMap x, w;
+};
+
+__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// 4-byte asynchronous copy to shared memory; zero when !valid (the address must be readable anyway).
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
+    const int n = valid ? 4 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void lt_tmem_ld16(uint32_t taddr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+
+// Persistent over the tiles, the row tiles of one weight tile first.  Warp 0: its lane 0 loads the
+// codes (TMA), its 32 lanes copy the stage's scales (their columns of the scale matrices); warp 1
+// issues the products; warps 2..9 sum and store.
+template <int BN>
+__global__ void __launch_bounds__(LT_THREADS, 1)
+    linear_tile_kernel(const __grid_constant__ LinearMaps maps, LinearTileArgs a, DevCtx ctx) {
+    using S = LtShape<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const int NS = a.n_stages;
+    uint8_t* scales = smem + (size_t)NS * S::kStage;
+    uint64_t* full = reinterpret_cast<uint64_t*>(scales + LT_SS * S::kScale);
+    uint64_t* empty = full + LT_MAX_STAGES;
+    uint64_t* pfull = empty + LT_MAX_STAGES;
+    uint64_t* pempty = pfull + S::kSlots;
+    uint64_t* sfull = pempty + S::kSlots;
+    uint64_t* sempty = sfull + LT_SS;
+    uint64_t* drain = sempty + LT_SS;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(drain + 1);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1) + 1;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const LinearArgs& l = a.l;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int p = 0; p < S::kSlots; ++p) {
+            mbar_init(smem_u32(&pfull[p]), 1);
+            mbar_init(smem_u32(&pempty[p]), LT_EPI);
+        }
+        for (int s = 0; s < LT_SS; ++s) {
+            mbar_init(smem_u32(&sfull[s]), 32);
+            mbar_init(smem_u32(&sempty[s]), LT_EPI);
+        }
+        mbar_init(smem_u32(drain), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&maps.x);
+        tma_prefetch_desc(&maps.w);
+    }
+    if (warp == 1) tmem_alloc(smem_u32(tmem_holder), S::kTmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    pdl_enter();
+
+    const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
+    if (warp == 0) {
+        const uint64_t pol = l2_policy_evict_last();
+        int stage = 0, ss = 0;
+        uint32_t phase = 0, sph = 0;
+        bool ok = true;
+        for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const int m0 = (int)(t % a.m_tiles) * LT_BM, n0 = (int)(t / a.m_tiles) * BN;
+            for (int ks = 0; ks < l.kb; ++ks) {
+                int good = 1;
+                if (lane == 0) {
+                    good = mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, ctx, abort_flag) &&
+                                   mbar_wait(smem_u32(&sempty[ss]), sph ^ 1u, ctx, abort_flag)
+                               ? 1
+                               : 0;
+                    if (good) {
+                        const uint32_t fb = smem_u32(&full[stage]);
+                        mbar_arrive_expect_tx(fb, S::kStage);
+                        const uint32_t dst = smem_u32(smem + (size_t)stage * S::kStage);
+                        tma_load_2d(dst, &maps.x, fb, ks * LT_KB, m0, pol);
+                        tma_load_2d(dst + LT_BM * LT_KB, &maps.w, fb, ks * LT_KB, n0, pol);
+                    }
+                }
+                if (!__shfl_sync(0xffffffffu, good, 0)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sd = smem_u32(scales + ss * S::kScale);
+#pragma unroll
+                for (int i = 0; i < LT_BM / 32; ++i) {
+                    const int r = i * 32 + lane;
+                    const bool in = m0 + r < l.M;
+                    cp_async4(sd + r * 4, l.xs + (int64_t)(in ? m0 + r : 0) * l.kb + ks, in);
+                }
+#pragma unroll
+                for (int i = 0; i < BN / 32; ++i) {
+                    const int r = i * 32 + lane;
+                    const bool in = n0 + r < l.N;
+                    cp_async4(sd + (LT_BM + r) * 4, l.ws + (int64_t)(in ? n0 + r : 0) * l.kb + ks, in);
+                }
+                cp_async_arrive(smem_u32(&sfull[ss]));
+                if (++stage == NS) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                if (++ss == LT_SS) {
+                    ss = 0;
+                    sph ^= 1u;
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!ok) {   // copies in flight land before the block may end
+            const uint64_t t0 = globaltimer();
+            while (globaltimer() - t0 < 200000ull) __nanosleep(1000);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = make_idesc(0u, LT_BM, BN);
+            int stage = 0, ps = 0;
+            uint32_t phase = 0, pph = 0;
+            bool ok = true, issued = false;
+            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                for (int ks = 0; ks < l.kb; ++ks) {
+                    if (!mbar_wait(smem_u32(&full[stage]), phase, ctx, abort_flag) ||
+                        !mbar_wait(smem_u32(&pempty[ps]), pph ^ 1u, ctx, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t xa = smem_u32(smem + (size_t)stage * S::kStage);
+                    const uint32_t wa = xa + LT_BM * LT_KB;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)   // the block's sum: the slot is overwritten first
+                        mma_ss<true>(tmem_base + ps * BN, sw128_desc(xa + kk * 32), sw128_desc(wa + kk * 32), idesc,
+                                     kk != 0 ? 1u : 0u);
+                    issued = true;
+                    mma_commit(smem_u32(&empty[stage]));
+                    mma_commit(smem_u32(&pfull[ps]));
+                    if (++stage == NS) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (++ps == S::kSlots) {
+                        ps = 0;
+                        pph ^= 1u;
+                    }
+                }
+            }
+            if (!ok && issued) {
+                mma_commit(smem_u32(drain));
+                mbar_wait_drain(smem_u32(drain), 0, ctx.timeout_ns);
+            }
+        }
+    } else {
+        const int quad = warp & 3;                        // TMEM lanes 32 quad ..
+        const int c0 = (warp - 2) / 4 * S::kCols;         // columns c0 .. c0 + kCols
+        constexpr int CH = S::kCols < 32 ? S::kCols : 32;
+        int ps = 0, ss = 0;
+        uint32_t pph = 0, sph = 0;
+        bool ok = true;
+        for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const int64_t m = (t % a.m_tiles) * LT_BM + quad * 32 + lane;
+            const int n0 = (int)(t / a.m_tiles) * BN + c0;
+            uint64_t acc[S::kCols / 2];
+#pragma unroll
+            for (int i = 0; i < S::kCols / 2; ++i) acc[i] = 0;
+            for (int ks = 0; ks < l.kb; ++ks) {
+                if (!mbar_wait_warp(smem_u32(&sfull[ss]), sph, ctx, abort_flag) ||
+                    !mbar_wait_warp(smem_u32(&pfull[ps]), pph, ctx, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float* sc = reinterpret_cast<const float*>(scales + ss * S::kScale);
+                const float sx = sc[quad * 32 + lane];
+                const uint64_t sx2 = f2_pack(sx, sx);
+                const float* sw = sc + LT_BM + c0;
+                const uint32_t ta = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(ps * BN + c0);
+#pragma unroll
+                for (int c = 0; c < S::kCols; c += CH) {
+                    uint32_t v[CH];
+                    lt_tmem_ld16(ta + c, v);
+                    if constexpr (CH == 32) lt_tmem_ld16(ta + c + 16, v + 16);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                    if (c + CH == S::kCols) {   // the last read of the slot: free it before the sums
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&pempty[ps]));
+                    }
+#pragma unroll
+                    for (int j = 0; j < CH; j += 4) {
+                        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(sw + c + j);
+                        const uint64_t p0 = f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                        const uint64_t p1 = f2_pack(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+                        acc[(c + j) / 2] = f2_fma(f2_mul(p0, w.x), sx2, acc[(c + j) / 2]);
+                        acc[(c + j) / 2 + 1] = f2_fma(f2_mul(p1, w.y), sx2, acc[(c + j) / 2 + 1]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sempty[ss]));
+                if (++ps == S::kSlots) {
+                    ps = 0;
+                    pph ^= 1u;
+                }
+                if (++ss == LT_SS) {
+                    ss = 0;
+                    sph ^= 1u;
+                }
+            }
+            if (!ok) break;
+            if (m < l.M) {
+                uint16_t* o = l.out + m * l.N + n0;
+#pragma unroll
+                for (int c = 0; c < S::kCols; c += 8) {
+                    if (n0 + c >= l.N) break;   // N is a multiple of 16
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float lo, hi;
+                        f2_unpack(acc[c / 2 + j], lo, hi);
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(lin_act(lo, l.relu2), lin_act(hi, l.relu2));
+                        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+                    }
+                    *reinterpret_cast<uint4*>(o + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, S::kTmem);
+    }
+}
+
+// ----------------------------------------------------------------------------- host
+
+template <int NT>
+static cudaError_t launch_linear_few(LinearFewArgs& a, int num_sms, const DevCtx& ctx, cudaStream_t stream) {
+    const size_t fixed = 2 * FwRed<NT>::kFloats * sizeof(float) + (FW_WARPS * FW_MAX_STAGES + 1) * 8 + 16;
+    a.n_stages = (int)std::min<size_t>(FW_MAX_STAGES, (FW_SMEM - fixed) / FW_WARPS / a.slot_bytes);
+    const size_t smem = (size_t)FW_WARPS * a.n_stages * a.slot_bytes + fixed;
+    auto k = linear_few_kernel<NT>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_k(k, dim3(num_sms), dim3(FW_THREADS), smem, stream, a, ctx);
+}
+
+template <int BN>
+static cudaError_t launch_linear_tiles(const LinearArgs& l, int num_sms, const DevCtx& ctx, cudaStream_t stream) {
+    using S = LtShape<BN>;
+    LinearMaps maps;
+    if (!make_map_u8_b128(&maps.x, l.xq, l.M, l.Kp, LT_BM) || !make_map_u8_b128(&maps.w, l.wq, l.N, l.Kp, BN))
+        return cudaErrorInvalidValue;
+    LinearTileArgs a = {};
+    a.l = l;
+    a.m_tiles = (int)((l.M + LT_BM - 1) / LT_BM);
+    a.n_tiles = (l.N + BN - 1) / BN;
+    const size_t fixed = 1024 + LT_SS * S::kScale + (2 * LT_MAX_STAGES + 2 * S::kSlots + 2 * LT_SS + 1) * 8 + 16;
+    a.n_stages = (int)std::min<size_t>(LT_MAX_STAGES, (FW_SMEM - fixed) / S::kStage);
+    const size_t smem = (size_t)a.n_stages * S::kStage + fixed;
+    auto k = linear_tile_kernel<BN>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = std::min<int64_t>((int64_t)a.m_tiles * a.n_tiles, num_sms);
+    return launch_k(k, dim3((unsigned)grid), dim3(LT_THREADS), smem, stream, maps, a, ctx);
+}
+
+static cudaError_t launch_linear(const LinearArgs& l, int num_sms, const DevCtx& ctx, cudaStream_t stream) {
+    if (l.M <= kFewMaxTokens) {
+        LinearFewArgs a = {};
+        a.l = l;
+        a.cut = fw_cut(l.Kp, 128);
+        a.share = fw_share(l.N, num_sms);
+        a.stride = fw_row_stride(a.cut.chunk);
+        a.slot_bytes = a.share.rows * a.stride;
+        return l.M <= 8 ? launch_linear_few<1>(a, num_sms, ctx, stream) : launch_linear_few<2>(a, num_sms, ctx, stream);
+    }
+    // the widest tile that still gives every SM one
+    const int64_t mt = (l.M + LT_BM - 1) / LT_BM;
+    auto fills = [&](int bn) { return mt * ((l.N + bn - 1) / bn) >= num_sms; };
+    if (fills(256)) return launch_linear_tiles<256>(l, num_sms, ctx, stream);
+    if (fills(128)) return launch_linear_tiles<128>(l, num_sms, ctx, stream);
+    if (fills(64)) return launch_linear_tiles<64>(l, num_sms, ctx, stream);
+    return launch_linear_tiles<32>(l, num_sms, ctx, stream);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_linear_fp8_b128(int64_t M, int32_t N, int32_t K, const uint8_t* x_codes, const float* x_scales,
+                               const uint8_t* w_codes, const float* w_scales, int32_t act, void* out, void* stream) {
+    if (M < 0 || M >= ((int64_t)1 << 31) - 128 || N < 16 || N > (1 << 20) || N % 16 != 0 || K < 16 || K > 65536 ||
+        K % 16 != 0)
+        return MOE_EINVAL;
+    if (act != MOE_ACT_NONE && act != MOE_ACT_RELU2) return MOE_EINVAL;
+    if (M == 0) return MOE_OK;
+    auto al = [](const void* p, uintptr_t n) { return p && reinterpret_cast<uintptr_t>(p) % n == 0; };
+    if (!al(x_codes, 16) || !al(w_codes, 16) || !al(out, 16) || !al(x_scales, 4) || !al(w_scales, 4))
+        return MOE_EINVAL;
+    DevCtx ctx;
+    int sms = 0;
+    const moe_status s = internal_device(&ctx, &sms);
+    if (s != MOE_OK) return s;
+    LinearArgs l = {};
+    l.xq = x_codes;
+    l.xs = x_scales;
+    l.wq = w_codes;
+    l.ws = w_scales;
+    l.out = static_cast<uint16_t*>(out);
+    l.M = M;
+    l.N = N;
+    l.kb = (K + 127) / 128;
+    l.Kp = l.kb * 128;
+    l.relu2 = act == MOE_ACT_RELU2;
+    return launch_linear(l, sms, ctx, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ECUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,281 @@
+// The norms between two blocks of the decoder, in one pass over the rows
+// (bloomery issue page, s.2: a hybrid decoder of pre-norm blocks; audio.cpp
+// model page, "Q4_K, Q3_K and Q2_K expert profiles": the model's normalisation).
+//
+//   n[t]  = y[t] / sqrt(mean(y[t]^2) + eps) * gain_post            norm after a block
+//   x'[t] = x[t] + alpha * gate (*) n[t]                           gate, residual scale, residual sum
+//   u[t]  = x'[t] / sqrt(mean(x'[t]^2) + eps) * gain_pre           norm before the next block
+//   codes, scales: u[t] as FP8_B128 (one fp32 scale amax / 448 per 128 values)
+//
+// Everything between the bf16 inputs and the one rounding of each output is
+// fp32: u and the codes come from the unrounded x', the codes from the
+// unrounded u.  A row is read once and stays in registers between its two
+// sums of squares.
+//
+// Bound: HBM bytes (about 8 bytes and 12 operations per value), latency at a
+// few rows.
+#include <algorithm>
+#include <cstdint>
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+
+struct NormArgs {
+    const uint16_t* y;          // block output (POST)
+    const uint16_t* gain_post;  // [H] or null (POST)
+    const uint16_t* gate;       // [H] or [T][H] or null (POST)
+    int64_t gate_ld;            // 0: one row for all tokens; H: a row per token
+    const uint16_t* x;          // residual stream
+    const uint16_t* gain_pre;   // [H] or null
+    uint16_t* x_out;            // POST
+    uint16_t* u;                // or null
+    uint8_t* codes;             // [T][Kp] or null
+    float* scales;              // [T][Kp / 128]
+    int64_t T;
+    int H;
+    float eps, alpha;
+};
+
+__device__ __forceinline__ void nm_unpack(const uint4& q, float (&f)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 nm_pack(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Sum over the block, the same bits in every thread: a butterfly in each warp, then the warps' sums
+// in warp order.  red: one float per warp, a buffer of its own per call between two barriers.
+__device__ __forceinline__ float nm_block_sum(float v, float* red, int n_warps) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (n_warps == 1) return v;
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+    __syncthreads();
+    float s = 0.0f;
+    for (int i = 0; i < n_warps; ++i) s += red[i];
+    return s;
+}
+
+// One block per row at a time (grid-stride); thread i holds the row's 16-byte vectors
+// i + j * blockDim.x, j < VPT.
+template <int VPT, bool POST, bool CODES>
+__global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
+    pdl_enter();
+    __shared__ float red[2][2][32];   // [row parity][sum][warp]
+    const int nv = a.H / 8;
+    const int kb = (a.H + 127) / 128;
+    const int n_warps = blockDim.x / 32;
+    int par = 0;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, par ^= 1) {
+        uint4 xq[VPT], yq[VPT];
+        const uint4* xr = reinterpret_cast<const uint4*>(a.x + t * a.H);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            xq[j] = v < nv ? xr[v] : make_uint4(0, 0, 0, 0);
+        }
+        float f[VPT][8];
+        if constexpr (POST) {
+            const uint4* yr = reinterpret_cast<const uint4*>(a.y + t * a.H);
+            float ss = 0.0f;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = threadIdx.x + j * blockDim.x;
+                yq[j] = v < nv ? yr[v] : make_uint4(0, 0, 0, 0);
+                nm_unpack(yq[j], f[j]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss = __fmaf_rn(f[j][i], f[j][i], ss);
+            }
+            ss = nm_block_sum(ss, red[par][0], n_warps);
+            const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)a.H), a.eps));
+            uint4* xo = reinterpret_cast<uint4*>(a.x_out + t * a.H);
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = threadIdx.x + j * blockDim.x;
+                if (v >= nv) break;
+                float p[8], xx[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[j][i] *= r;
+                if (a.gain_post) {
+                    nm_unpack(reinterpret_cast<const uint4*>(a.gain_post)[v], p);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[j][i] *= p[i];
+                }
+                if (a.gate) {
+                    nm_unpack(reinterpret_cast<const uint4*>(a.gate + t * a.gate_ld)[v], p);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[j][i] *= p[i];
+                }
+                nm_unpack(xq[j], xx);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[j][i] = __fmaf_rn(a.alpha, f[j][i], xx[i]);
+                xo[v] = nm_pack(f[j]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) nm_unpack(xq[j], f[j]);
+        }
+        if (!a.u && !CODES) continue;
+        float ss = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = __fmaf_rn(f[j][i], f[j][i], ss);
+        ss = nm_block_sum(ss, red[par][1], n_warps);
+        const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)a.H), a.eps));
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[j][i] *= r;
+            if (a.gain_pre && v < nv) {
+                float p[8];
+                nm_unpack(reinterpret_cast<const uint4*>(a.gain_pre)[v], p);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[j][i] *= p[i];
+            }
+            if (a.u && v < nv) reinterpret_cast<uint4*>(a.u + t * a.H)[v] = nm_pack(f[j]);
+            if constexpr (CODES) {
+                // a block of 128 values is 16 neighbouring lanes (vectors past the row are zero)
+                float m = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[j][i]));
+#pragma unroll
+                for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                const float s = m > 0.0f ? __fdiv_rn(m, 448.0f) : 1.0f;
+                if (v < kb * 16) {
+                    uint32_t c[2] = {0, 0};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        c[i / 4] |= (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(f[j][i], s), __NV_SATFINITE, __NV_E4M3)
+                                    << (8 * (i % 4));
+                    *reinterpret_cast<uint2*>(a.codes + (t * kb * 16 + v) * 8) = make_uint2(c[0], c[1]);
+                    if (v % 16 == 0) a.scales[t * kb + v / 16] = s;
+                }
+            }
+        }
+    }
+}
+
+// ----------------------------------------------------------------------------- host
+
+template <int VPT>
+static cudaError_t launch_vpt(const NormArgs& a, int threads, int num_sms, cudaStream_t stream) {
+    const bool post = a.y != nullptr, codes = a.codes != nullptr;
+    void (*k)(NormArgs) = post ? (codes ? norm_kernel<VPT, true, true> : norm_kernel<VPT, true, false>)
+                               : (codes ? norm_kernel<VPT, false, true> : norm_kernel<VPT, false, false>);
+    int per_sm = 0;
+    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, 0);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = std::min(a.T, (int64_t)num_sms * std::max(per_sm, 1));
+    return launch_k(k, dim3((unsigned)grid), dim3((unsigned)threads), 0, stream, a);
+}
+
+static cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t stream) {
+    // vectors of a row, a whole number of 128-value blocks
+    const int nv = (a.H + 127) / 128 * 16;
+    int vpt = 1;
+    while ((nv + vpt - 1) / vpt > 1024) vpt *= 2;
+    const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
+    switch (vpt) {
+        case 1: return launch_vpt<1>(a, threads, num_sms, stream);
+        case 2: return launch_vpt<2>(a, threads, num_sms, stream);
+        case 4: return launch_vpt<4>(a, threads, num_sms, stream);
+        default: return launch_vpt<8>(a, threads, num_sms, stream);
+    }
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+namespace {
+bool is_aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+moe_status run_norm(const NormArgs& a, void* stream) {
+    DevCtx ctx;
+    int sms = 0;
+    const moe_status s = internal_device(&ctx, &sms);
+    if (s != MOE_OK) return s;
+    return launch_norm(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ECUDA;
+}
+
+moe_status check_norm(int64_t T, int32_t H, float eps) {
+    if (T < 0 || T >= ((int64_t)1 << 31) || H < 16 || H > 65536 || H % 16 != 0) return MOE_EINVAL;
+    return eps >= 0.0f && eps < 3.4e38f ? MOE_OK : MOE_EINVAL;
+}
+
+bool codes_ok(const uint8_t* codes, const float* scales) {
+    return !codes == !scales && is_aligned(codes, 16) && is_aligned(scales, 4);
+}
+}  // namespace
+
+extern "C" {
+
+moe_status moe_prenorm(int64_t T, int32_t H, float eps, const void* x, const void* gain, void* u, uint8_t* codes,
+                       float* scales, void* stream) {
+    const moe_status s = check_norm(T, H, eps);
+    if (s != MOE_OK) return s;
+    if (T == 0) return MOE_OK;
+    if (!x || (!u && !codes) || !codes_ok(codes, scales)) return MOE_EINVAL;
+    if (!is_aligned(x, 16) || !is_aligned(gain, 16) || !is_aligned(u, 16)) return MOE_EINVAL;
+    NormArgs a = {};
+    a.x = static_cast<const uint16_t*>(x);
+    a.gain_pre = static_cast<const uint16_t*>(gain);
+    a.u = static_cast<uint16_t*>(u);
+    a.codes = codes;
+    a.scales = scales;
+    a.T = T;
+    a.H = H;
+    a.eps = eps;
+    return run_norm(a, stream);
+}
+
+moe_status moe_postnorm(int64_t T, int32_t H, float eps, float alpha, const void* y, const void* gain,
+                        const void* gate, int64_t gate_ld, const void* x, void* x_out, const void* next_gain, void* u,
+                        uint8_t* codes, float* scales, void* stream) {
+    const moe_status s = check_norm(T, H, eps);
+    if (s != MOE_OK) return s;
+    if (!(alpha > -3.4e38f && alpha < 3.4e38f)) return MOE_EINVAL;
+    if (gate && gate_ld != 0 && gate_ld != H) return MOE_EINVAL;
+    if (T == 0) return MOE_OK;
+    if (!y || !x || !x_out || x_out == u || !codes_ok(codes, scales)) return MOE_EINVAL;
+    if (!is_aligned(y, 16) || !is_aligned(gain, 16) || !is_aligned(gate, 16) || !is_aligned(x, 16) ||
+        !is_aligned(x_out, 16) || !is_aligned(next_gain, 16) || !is_aligned(u, 16))
+        return MOE_EINVAL;
+    NormArgs a = {};
+    a.y = static_cast<const uint16_t*>(y);
+    a.gain_post = static_cast<const uint16_t*>(gain);
+    a.gate = static_cast<const uint16_t*>(gate);
+    a.gate_ld = gate_ld;
+    a.x = static_cast<const uint16_t*>(x);
+    a.gain_pre = static_cast<const uint16_t*>(next_gain);
+    a.x_out = static_cast<uint16_t*>(x_out);
+    a.u = static_cast<uint16_t*>(u);
+    a.codes = codes;
+    a.scales = scales;
+    a.T = T;
+    a.H = H;
+    a.eps = eps;
+    a.alpha = alpha;
+    return run_norm(a, stream);
+}
+
+}  // extern "C"
