@@ -12,10 +12,10 @@
 //    further blocks write the E4M3 codes of x.  It zeroes the second kernel's counters.
 // 2. few_layer_kernel, persistent, one CTA of eight warps per SM: every CTA ranks the logits itself
 //    (the same integers give the same choice everywhere), lists the touched experts, and then its
-//    warps stream weights (few.cuh): up pieces (9 or 10 rows of one expert, claimed by single warps),
+//    consumer warps stream weights (few.cuh): up pieces (16 rows of one expert, claimed for single warps),
 //    then the CTA's share of the output rows through all touched experts, so that the weighted sum
-//    over experts, the residual and the one rounding happen in the CTA that holds them.  A warp
-//    without further up pieces fills its ring with down weights while the last pieces report.
+//    over experts, the residual and the one rounding happen in the CTA that holds them.  The
+//    ring of a warp without further up pieces takes down weights while the last pieces report.
 //
 // Up pieces are claimed from a counter, so those that a warp waits for belong to warps that run and
 // that wait for nothing; no CTA needs another to be resident, and every wait is bounded.
@@ -33,9 +33,6 @@
 namespace moe {
 
 constexpr int FEW_RT = 256;          // threads of the router kernel
-constexpr int FEW_PQ = 8;            // claimed pieces of a warp: its ring's, and the next one
-static_assert(FEW_PQ > FW_MAX_STAGES, "a piece has one stage at least");
-constexpr int FEW_ABSENT = 0xFFFF;   // token not routed to the expert
 
 // ----------------------------------------------------------------------------- router
 
@@ -137,10 +134,6 @@ struct FewArgs {
     float* topk_w;              // or null
     const long long* logits;
     const uint8_t* act;         // up operand rows: x, or its E4M3 codes
-    const uint8_t* w_up;
-    const uint8_t* w_down;
-    const uint8_t* w_up_s;      // shared expert (bf16): [ns F][H]
-    const uint8_t* w_down_s;    // [H][ns F]
     const float* su;            // E4M3: [E]; B128: [E][F][kbu]
     const float* sd;            // E4M3: [E]; B128: [E][H][kbd]
     float x_scale, h_scale;
@@ -149,17 +142,26 @@ struct FewArgs {
     int* counters;
     int T, H, E, K, F, ns;
     FwCut up, down;
-    FwShare share;              // of the output rows; its `rows` also bound an up piece
-    int stride, slot_bytes, n_stages;
+    FwShare share;              // of the output rows
+    int slot_bytes, n_stages;
     int n_list_max;
     int hold;                   // test hook: up piece 0 never reports
 };
 
-// shared memory after the rings: reduction buffers | wt [n][16] f32 | lst_e [n] i32 | rowi [n][16] u16 |
-// emask [256] i32 | slot [256] i32 | sel_w [16][16] f32 | sel_e [16][16] i32 | barriers | piece queues | flags
+// Weight matrices: rows of W_up in boxes of 16; rows of W_down in boxes of share.rows and one less;
+// the same of the shared expert.
+struct FewMaps {
+    CUtensorMap up, down[2], up_s, down_s[2];
+};
+
+constexpr int FEW_PIECE = 16;   // rows of an up piece (F is a multiple of 16)
+
+// shared memory after the rings: reduction buffers | wt [n][16] f32 | rowi [n][16] u16 | tok [n][16] u8 |
+// lst_e [n] i32 | lst_n [n] i32 | emask [256] i32 | slot [256] i32 | sel_w [16][16] f32 | sel_e [16][16] i32 |
+// barriers | piece of each slot | flags
 __host__ __device__ inline size_t few_table_bytes(int n_list) {
-    return (size_t)n_list * (64 + 4 + 32) + 16 + 4 * 1024 + (FW_WARPS * FW_MAX_STAGES + 1) * 8 + FW_WARPS * FEW_PQ * 4 +
-           16;
+    return (size_t)n_list * (64 + 32 + 16 + 8) + 16 + 4 * 1024 + FwRings::kBarBytes + 8 +
+           FW_WARPS * FW_MAX_STAGES * 4 + 16;
 }
 
 // The K best experts of one token (one warp): by logit, ties to the lower index; lane k returns the
@@ -208,22 +210,204 @@ __device__ __forceinline__ void few_select(const long long* row, int E, int K, i
     my_w = ex / z;
 }
 
-template <int FMT, int NT>
-__global__ void __launch_bounds__(FW_THREADS, 1) few_layer_kernel(FewArgs a, DevCtx ctx) {
+// One up piece: 16 rows of a list entry with at most 8 TT tokens.
+template <int FMT, int TT>
+__device__ __forceinline__ bool few_up(const FewArgs& a, FwTake& ring, int e, int f, int n_tok, const uint16_t* rowi,
+                                       const uint8_t* tok, const DevCtx& ctx, volatile int* abort) {
     constexpr bool BF16 = FMT == MOE_BF16, BLOCK = FMT == MOE_FP8_B128;
     constexpr int ES = BF16 ? 2 : 1;
+    const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
+    FwSide<2> side;
+#pragma unroll
+    for (int t = 0; t < TT; ++t) side.act[t] = a.act + (int64_t)tok[min(t * 8 + g, n_tok - 1)] * a.H * ES + q * 16;
+    if constexpr (BLOCK) {
+        const int kb = a.up.bytes / 128;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) side.ws[nt][j] = a.su + ((int64_t)e * a.F + f + nt * 8 + 2 * q + j) * kb;
+    }
+    FwAcc<2> acc;
+    acc.clear();
+    FwActs<2, TT == 2, BLOCK, false> v;
+    fw_fetch(v, side, 0, a.H * ES);
+    for (int c0 = 0; c0 < a.up.bytes;) {
+        if (!ring.wait(ctx, abort)) return false;
+        fw_mul<BF16>(acc, ring.data(), FEW_PIECE, v);
+        ring.release();
+        c0 += a.up.chunk;
+        if (c0 < a.up.bytes) fw_fetch(v, side, c0, a.H * ES);
+    }
+    const float sc = BF16 ? 1.0f : BLOCK ? a.x_scale : __fmul_rn(a.su[e], a.x_scale);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        if (t * 8 + g >= n_tok) continue;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            const int64_t o = (int64_t)rowi[t * 8 + g] * a.F + f + nt * 8 + 2 * q;
+            float h[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float z = acc.sum(nt, 2 * t + j);
+                if constexpr (!BF16) z = __fmul_rn(z, sc);
+                h[j] = z <= 0.0f ? 0.0f : __fmul_rn(z, z);   // a NaN stays one
+            }
+            if constexpr (BF16) {
+                // h as the sum of two bf16, 16 bits of it: one alone would add a second rounding of the
+                // output's size
+                const __nv_bfloat162 hi = __floats2bfloat162_rn(h[0], h[1]);
+                const float t0 = __low2float(hi), t1 = __high2float(hi), inf = __uint_as_float(0x7f800000u);
+                *reinterpret_cast<__nv_bfloat162*>(a.h + 2 * o) = hi;
+                *reinterpret_cast<__nv_bfloat162*>(a.h + a.h_lo + 2 * o) =
+                    __floats2bfloat162_rn(t0 < inf ? __fsub_rn(h[0], t0) : 0.0f, t1 < inf ? __fsub_rn(h[1], t1) : 0.0f);
+            } else {
+                const uint32_t c0 = __nv_cvt_float_to_fp8(__fdiv_rn(h[0], a.h_scale), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t c1 = __nv_cvt_float_to_fp8(__fdiv_rn(h[1], a.h_scale), __NV_SATFINITE, __NV_E4M3);
+                *reinterpret_cast<uint16_t*>(a.h + o) = (uint16_t)(c0 | (c1 << 8));
+            }
+        }
+    }
+    return true;
+}
+
+// One warp's part of n output rows from d0 on, through its pairs of all list entries: the weighted sums
+// tot [token][row] (shared memory, this warp's).
+template <int FMT>
+struct FewDown {
+    static constexpr bool BF16 = FMT == MOE_BF16, BLOCK = FMT == MOE_FP8_B128;
+    static constexpr int ES = BF16 ? 2 : 1;
+    const FewArgs& a;
+    FwTake& ring;
+    const int *lst_e, *lst_n;
+    const uint16_t* rowi;
+    const uint8_t* tok;
+    const float* wt;
+    int n_list, warp, d0, n;
+    float* tot;
+    const DevCtx& ctx;
+    volatile int* abort;
+
+    // Entry i: activation rows (lo: bf16 low parts), weight scales
+    template <int TT>
+    __device__ __forceinline__ void point(FwSide<3>& side, int i, int64_t lo) const {
+        const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
+        const int last = lst_n[i] - 1;
+        side.act[0] = a.h + (int64_t)rowi[i * 16 + min(g, last)] * a.F * ES + q * 16 + lo;
+        if constexpr (TT == 2) side.act[1] = a.h + (int64_t)rowi[i * 16 + min(8 + g, last)] * a.F * ES + q * 16 + lo;
+        else if constexpr (BF16) side.act[1] = side.act[0] + a.h_lo;   // the low parts are rows 8 .. 15
+        if constexpr (BLOCK) {
+            const int kb = a.down.bytes / 128;
+#pragma unroll
+            for (int nt = 0; nt < 3; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    side.ws[nt][j] = a.sd + ((int64_t)lst_e[i] * a.H + d0 + min(nt * 8 + 2 * q + j, n - 1)) * kb;
+        }
+    }
+    // Weighted sums of entry i, for the tokens routed to it only
+    template <int TT>
+    __device__ __forceinline__ void add(const FwAcc<3>& acc, int i) const {
+        const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
+        const float sc = FMT == MOE_FP8_E4M3 ? a.sd[lst_e[i]] : 1.0f;
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const int s = t * 8 + g;
+            if (s >= lst_n[i]) continue;
+            const float w = wt[i * 16 + s] * sc;
+#pragma unroll
+            for (int nt = 0; nt < 3; ++nt) {
+                float2* p = reinterpret_cast<float2*>(tot + tok[i * 16 + s] * FW_ROWS + nt * 8 + 2 * q);
+                float2 v = *p;
+                float y0 = acc.sum(nt, 2 * t), y1 = acc.sum(nt, 2 * t + 1);
+                if constexpr (BF16 && TT == 1) {
+                    y0 += acc.sum(nt, 2);
+                    y1 += acc.sum(nt, 3);
+                }
+                v.x = __fmaf_rn(w, y0, v.x);
+                v.y = __fmaf_rn(w, y1, v.y);
+                *p = v;
+            }
+        }
+        __syncwarp();
+    }
+    // An entry with more than eight tokens
+    __device__ __forceinline__ bool wide(FwPairs& pr) {
+        const int i = pr.i;
+        FwSide<3> hi, lo;
+        point<2>(hi, i, 0);
+        if constexpr (BF16) point<2>(lo, i, a.h_lo);
+        FwAcc<3> acc;
+        acc.clear();
+        do {
+            FwActs<3, true, BLOCK, false> v;
+            fw_fetch(v, hi, pr.k * a.down.chunk, a.F * ES);
+            if (!ring.wait(ctx, abort)) return false;
+            fw_mul<BF16>(acc, ring.data(), n, v);
+            if constexpr (BF16) {
+                fw_fetch(v, lo, pr.k * a.down.chunk, a.F * ES);
+                fw_mul<BF16>(acc, ring.data(), n, v);
+            }
+            ring.release();
+            pr.step(lst_e, n_list, a.down.n, warp);
+        } while (pr.i == i);
+        add<2>(acc, i);
+        return true;
+    }
+    __device__ __forceinline__ bool run() {
+        FwPairs pr{0, 0};
+        pr.seek(lst_e, n_list, a.down.n, warp);
+        bool fetched = false;
+        FwSide<3> side;
+        FwActs<3, BF16, BLOCK, false> v;
+        while (pr.i < n_list) {
+            const int i = pr.i;
+            if (lst_n[i] > 8) {
+                if (!wide(pr)) return false;
+                continue;
+            }
+            if (!fetched) {
+                point<1>(side, i, 0);
+                fw_fetch(v, side, pr.k * a.down.chunk, a.F * ES);
+            }
+            FwAcc<3> acc;
+            acc.clear();
+            do {
+                if (!ring.wait(ctx, abort)) return false;
+                fw_mul<BF16>(acc, ring.data(), n, v);
+                ring.release();
+                // the next pair's activations, of this entry or the next
+                pr.step(lst_e, n_list, a.down.n, warp);
+                fetched = pr.i < n_list && lst_n[pr.i] <= 8;
+                if (fetched) {
+                    if (pr.i != i) point<1>(side, pr.i, 0);
+                    fw_fetch(v, side, pr.k * a.down.chunk, a.F * ES);
+                }
+            } while (pr.i == i);
+            add<1>(acc, i);
+        }
+        return true;
+    }
+};
+
+template <int FMT>
+__global__ void __launch_bounds__(FW_THREADS, 1)
+    few_layer_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs a, DevCtx ctx) {
+    constexpr int ES = FMT == MOE_BF16 ? 2 : 1;
     extern __shared__ __align__(1024) uint8_t few_smem[];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     uint8_t* p = few_smem + (size_t)FW_WARPS * a.n_stages * a.slot_bytes;
-    FwRed<NT> red;
+    FwRed red;
     red.buf = reinterpret_cast<float*>(p);
-    p += 2 * FwRed<NT>::kFloats * sizeof(float);
+    p += FwRed::bytes(a.share.units);
     float* wt = reinterpret_cast<float*>(p);
     p += (size_t)a.n_list_max * 64;
     uint16_t* rowi = reinterpret_cast<uint16_t*>(p);
     p += (size_t)a.n_list_max * 32;
+    uint8_t* tok = p;
+    p += (size_t)a.n_list_max * 16;
     int* lst_e = reinterpret_cast<int*>(p);
-    p += ((size_t)a.n_list_max * 4 + 15) / 16 * 16;
+    int* lst_n = lst_e + a.n_list_max;
+    p += ((size_t)a.n_list_max * 8 + 15) / 16 * 16;
     int* emask = reinterpret_cast<int*>(p);
     p += 1024;
     int* eslot = reinterpret_cast<int*>(p);
@@ -232,36 +416,34 @@ __global__ void __launch_bounds__(FW_THREADS, 1) few_layer_kernel(FewArgs a, Dev
     p += 1024;
     int(*sel_e)[16] = reinterpret_cast<int(*)[16]>(p);
     p += 1024;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(p);
-    uint64_t* rbar = bars + FW_WARPS * FW_MAX_STAGES;
-    int* pieces = reinterpret_cast<int*>(rbar + 1) + warp * FEW_PQ;
-    volatile int* abort_flag = reinterpret_cast<int*>(rbar + 1) + FW_WARPS * FEW_PQ;
+    FwRings rings;
+    rings.base = few_smem;
+    rings.full = reinterpret_cast<uint64_t*>(p);
+    rings.empty = rings.full + FW_WARPS * FW_MAX_STAGES;
+    rings.slot_bytes = a.slot_bytes;
+    rings.n = a.n_stages;
+    uint64_t* rbar = rings.full + FwRings::kBarBytes / 8;
+    volatile int* slot_piece = reinterpret_cast<volatile int*>(rbar + 1);   // [warp][slot]
+    volatile int* abort_flag = slot_piece + FW_WARPS * FW_MAX_STAGES;
     int* n_touched = const_cast<int*>(abort_flag) + 1;
     red.bar = smem_u32(rbar);
     red.turn = 0;
-    FwRing ring;
-    ring.base = smem_u32(few_smem) + warp * a.n_stages * a.slot_bytes;
-    ring.bars = smem_u32(bars + warp * FW_MAX_STAGES);
-    ring.slot_bytes = a.slot_bytes;
-    ring.stride = a.stride;
-    ring.n = a.n_stages;
-    ring.put = ring.take = 0;
-    ring.parity = 0;
-    ring.policy = l2_policy_evict_first();
 
-    if (lane == 0)
-        for (int s = 0; s < a.n_stages; ++s) mbar_init(ring.bars + 8 * s, 1);
     if (tid == 0) {
+        rings.init();
         mbar_init(smem_u32(rbar), FW_WARPS);
         *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&maps.up);
+        tma_prefetch_desc(&maps.down[0]);
+        tma_prefetch_desc(&maps.down[1]);
     }
-    if (lane == 0) fence_mbar_init();
     for (int i = tid; i < 256; i += FW_THREADS) emask[i] = 0;
     __syncthreads();
     pdl_enter();
 
     // ---- the routing, the same in every CTA
-    for (int t = warp; t < a.T; t += FW_WARPS) {
+    for (int t = warp; t < a.T; t += FW_WARPS + 1) {
         int e;
         float w;
         few_select(a.logits + (int64_t)t * a.E, a.E, a.K, lane, e, w);
@@ -276,172 +458,134 @@ __global__ void __launch_bounds__(FW_THREADS, 1) few_layer_kernel(FewArgs a, Dev
         }
     }
     __syncthreads();
-    if (warp == 0) {   // the touched experts, ascending
+    if (warp == 0) {   // the touched experts, ascending, then the shared expert's chunks
         int n = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             const int e = e0 + lane;
-            const bool on = e < a.E && emask[e] != 0;
-            const uint32_t m = __ballot_sync(0xffffffffu, on);
-            if (on) {
+            const int mask = e < a.E ? emask[e] : 0;
+            const uint32_t m = __ballot_sync(0xffffffffu, mask != 0);
+            if (mask) {
                 const int i = n + __popc(m & ((1u << lane) - 1u));
                 eslot[e] = i;
                 lst_e[i] = e;
+                lst_n[i] = __popc(mask);
             }
             n += __popc(m);
         }
-        if (lane < a.ns) lst_e[n + lane] = a.E + lane;
+        if (lane < a.ns) {
+            lst_e[n + lane] = a.E + lane;
+            lst_n[n + lane] = a.T;
+        }
         if (lane == 0) *n_touched = n;
     }
     __syncthreads();
     const int n_routed = *n_touched, n_list = n_routed + a.ns;
-    for (int i = tid; i < n_list * 16; i += FW_THREADS) {
-        const int j = i / 16 - n_routed, t = i % 16;   // j >= 0: chunk j of the shared expert, every token
-        const bool on = j >= 0 && t < a.T;
-        rowi[i] = (uint16_t)(on ? a.T * a.K + j * a.T + t : FEW_ABSENT);
-        wt[i] = on ? 1.0f : 0.0f;
-    }
-    __syncthreads();
-    for (int i = tid; i < a.T * a.K; i += FW_THREADS) {
-        const int t = i / a.K, k = i % a.K;
-        const int s = eslot[sel_e[t][k]] * 16 + t;
-        rowi[s] = (uint16_t)i;
-        wt[s] = sel_w[t][k];
+    // each list entry's tokens, ascending, with the row of h and the weight that go with them
+    for (int i = tid; i < a.T * (a.K + a.ns); i += FW_THREADS) {
+        const int t = i % a.T, k = i / a.T;
+        int s, row;
+        float w;
+        if (k < a.K) {
+            const int e = sel_e[t][k];
+            s = eslot[e] * 16 + __popc(emask[e] & ((1 << t) - 1));
+            row = t * a.K + k;
+            w = sel_w[t][k];
+        } else {
+            s = (n_routed + k - a.K) * 16 + t;
+            row = a.T * a.K + (k - a.K) * a.T + t;
+            w = 1.0f;
+        }
+        rowi[s] = (uint16_t)row;
+        tok[s] = (uint8_t)t;
+        wt[s] = w;
     }
     __syncthreads();
 
-    // ---- work: each expert's F rows in `per` equal pieces, as many pieces in all as fill a whole
-    // number of rounds over the grid's warps
-    const int n_warps = gridDim.x * FW_WARPS;
-    const int rounds = (int)(((int64_t)n_list * a.F + (int64_t)n_warps * a.share.rows - 1) / ((int64_t)n_warps * a.share.rows));
-    const int per = min(a.F, max(rounds * n_warps / n_list, (a.F + a.share.rows - 1) / a.share.rows));
-    const int n_pieces = n_list * per;
-    auto piece_row = [&](int j) { return (int)((int64_t)j * a.F / per); };
-    // output rows: unit u's group starts at
-    const int n_groups = gridDim.x * a.share.units * a.share.groups;
-    const int my_group = warp * a.share.groups / FW_WARPS, gw = FW_WARPS / a.share.groups, wk = warp % gw;
-    auto group_row = [&](int u, int grp) { return (int)((int64_t)(u * a.share.groups + grp) * a.H / n_groups); };
+    // ---- work
+    const int per = a.F / FEW_PIECE, n_pieces = n_list * per;   // pieces of one expert, of all
+    const int n_units = gridDim.x * a.share.units;
+    auto unit_row = [&](int u) { return (int)((int64_t)u * a.H / n_units); };
 
-    // ---- filling the ring, stage by stage: this warp's up pieces, then its pairs of every unit
-    const uint8_t* f_src = nullptr;      // the rows being filled, ld apart
-    int64_t f_ld = 0;
-    int f_n = 0, f_k = a.up.n;           // their number, and the next chunk
-    int f_queue = 0, claim = 0;          // pieces queued so far; the next piece (lane 0)
-    int f_unit = -1, f_d0 = 0;           // the output unit being filled (-1: still in up pieces), its first row
-    FwPairs f_pair{0, 0};
-    int f_i = -1;                        // the expert that f_src belongs to
-    if (lane == 0) claim = atomicAdd(a.counters, 1);
-    auto next_unit = [&]() {
-        ++f_unit;
-        f_i = -1;
-        f_pair.i = 0;
-        f_pair.seek(n_list, a.down.n, wk, gw);
-        const int u = blockIdx.x * a.share.units + f_unit;
-        f_d0 = group_row(u, my_group);
-        f_n = group_row(u, my_group + 1) - f_d0;
-    };
-    auto fill_next = [&]() {
-        if (f_unit < 0) {
-            if (f_k == a.up.n) {
-                const int piece = __shfl_sync(0xffffffffu, claim, 0);
-                if (lane == 0) pieces[f_queue % FEW_PQ] = piece;
-                ++f_queue;
-                __syncwarp();
-                if (piece < n_pieces) {
-                    const int i = piece / per, j = piece - i * per, f = piece_row(j);
-                    f_n = piece_row(j + 1) - f;
-                    f_k = 0;
-                    const int e = lst_e[i];
-                    f_src = e < a.E ? a.w_up + ((int64_t)e * a.F + f) * a.up.bytes
-                                    : a.w_up_s + ((int64_t)(e - a.E) * a.F + f) * a.up.bytes;
-                } else {
-                    next_unit();
+    // A CTA's first pieces are claimed together, an equal share for every CTA and one more while there
+    // are any: single claims would let the CTAs that start first take more than others.
+    const int first = min(n_pieces / (int)gridDim.x, FW_WARPS);
+    if (tid == 0) *n_touched = first > 0 ? atomicAdd(a.counters, first) : 0;
+    __syncthreads();
+
+    if (warp == FW_WARPS) {
+        // ---- producer: lane w fills ring w stage by stage, its pieces and then its pairs of every unit
+        const uint64_t policy = l2_policy_evict_first();
+        const int w = lane % FW_WARPS;
+        FwPut put(rings, w);
+        volatile int* my_piece = slot_piece + w * FW_MAX_STAGES;
+        int y = 0, x = a.up.bytes, n = 0, piece = 0;   // the rows and the byte to fill next
+        int claim = w < first ? *n_touched + w : n_pieces;
+        const bool active = lane < FW_WARPS;
+        if (active && w == first) claim = atomicAdd(a.counters, 1);
+        int unit = -1;                                 // output unit (-1: still in pieces)
+        const CUtensorMap* map = nullptr;
+        FwPairs pr{0, 0};
+        auto next_unit = [&]() {   // to the next output unit with something for this ring
+            do {
+                if (++unit == a.share.units) return false;
+                const int u = blockIdx.x * a.share.units + unit;
+                y = unit_row(u);
+                n = unit_row(u + 1) - y;
+                pr.i = 0;
+                pr.seek(lst_e, n_list, a.down.n, w);
+            } while (n <= 0 || pr.i >= n_list);
+            return true;
+        };
+        auto step = [&]() {
+            if (unit < 0) {
+                if (x >= a.up.bytes) {
+                    piece = claim;
+                    if (piece >= n_pieces) {   // the consumer's sign that there is no further piece
+                        my_piece[put.slot] = n_pieces;
+                        put.mark();
+                        return next_unit();
+                    }
+                    const int i = piece / per, e = lst_e[i], f = (piece - i * per) * FEW_PIECE;
+                    x = 0;
+                    map = e < a.E ? &maps.up : &maps.up_s;
+                    y = (e < a.E ? e : e - a.E) * a.F + f;
                 }
-            }
-            if (f_unit < 0) {
-                ring.fill(f_src + f_k * a.up.chunk, a.up.bytes, f_n,
-                          (uint32_t)min(a.up.chunk, a.up.bytes - f_k * a.up.chunk));
+                my_piece[put.slot] = piece;
+                put.fill(map, x, y, FEW_PIECE * a.up.chunk, policy);
+                x += a.up.chunk;
                 // the next piece is claimed one stage before it is needed
-                if (++f_k == a.up.n && lane == 0) claim = atomicAdd(a.counters, 1);
-                return;
+                if (x >= a.up.bytes) claim = atomicAdd(a.counters, 1);
+                return true;
             }
-        }
-        while (f_unit < a.share.units) {
-            if (f_pair.i < n_list && f_n > 0) {
-                if (f_pair.i != f_i) {
-                    f_i = f_pair.i;
-                    const int e = lst_e[f_i];
-                    f_ld = e < a.E ? (int64_t)a.down.bytes : (int64_t)a.ns * a.F * ES;
-                    f_src = e < a.E ? a.w_down + ((int64_t)e * a.H + f_d0) * f_ld
-                                    : a.w_down_s + (int64_t)f_d0 * f_ld + (int64_t)(e - a.E) * a.F * ES;
-                }
-                ring.fill(f_src + f_pair.k * a.down.chunk, f_ld, f_n,
-                          (uint32_t)min(a.down.chunk, a.down.bytes - f_pair.k * a.down.chunk));
-                f_pair.step(n_list, a.down.n, wk, gw);
-                return;
-            }
-            next_unit();
-        }
-    };
-    for (int s = 0; s < a.n_stages; ++s) fill_next();
+            const int e = lst_e[pr.i], one_less = a.share.rows - n;   // 0 or 1
+            // chunk j of the shared expert: columns from j F on (past j's end: the next chunk's weights,
+            // which meet activations of zero)
+            if (e < a.E)
+                put.fill(&maps.down[one_less], pr.k * a.down.chunk, e * a.H + y, n * a.down.chunk, policy);
+            else
+                put.fill(&maps.down_s[one_less], (e - a.E) * a.F * ES + pr.k * a.down.chunk, y, n * a.down.chunk, policy);
+            pr.step(lst_e, n_list, a.down.n, w);
+            return pr.i < n_list || next_unit();
+        };
+        if (!fw_produce(put, active, step, ctx, abort_flag)) fw_settle();
+        return;
+    }
 
-    const int g = lane / 4, q = lane % 4;
-    // ---- up pieces
-    for (int c_queue = 0;; ++c_queue) {
-        const int piece = pieces[c_queue % FEW_PQ];
-        if (piece >= n_pieces) break;
-        const int i = piece / per, f = piece_row(piece % per), n = piece_row(piece % per + 1) - f;
-        const int e = lst_e[i];
-        FwRows<NT> act;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            act.on[nt] = rowi[i * 16 + nt * 8 + g] != FEW_ABSENT;
-            act.p[nt] = a.act + (int64_t)(nt * 8 + g) * a.H * ES + q * 16;
+    // ---- consumers: pieces
+    FwTake ring(rings, warp);
+    while (true) {
+        if (!ring.wait(ctx, abort_flag)) return fw_settle();
+        const int piece = slot_piece[warp * FW_MAX_STAGES + ring.slot];
+        if (piece >= n_pieces) {
+            ring.release();
+            break;
         }
-        const int kb = a.up.bytes / 128;
-        const float* ws0 = BLOCK ? a.su + ((int64_t)e * a.F + f + min(g, n - 1)) * kb : nullptr;
-        const float* ws1 = BLOCK ? a.su + ((int64_t)e * a.F + f + min(g + 8, n - 1)) * kb : nullptr;
-        float acc[NT][4] = {};
-        for (int k = 0; k < a.up.n; ++k) {
-            const int c0 = k * a.up.chunk, bytes = min(a.up.chunk, a.up.bytes - c0);
-            auto load = [&](auto& v, int seg0, int n_seg) {
-                const int off = c0 + seg0 * FW_SEG;
-                fw_load(v, act, off, n_seg, a.H * ES, 0);
-                if constexpr (BLOCK) {
-#pragma unroll
-                    for (int s = 0; s < FW_GROUP / 2; ++s)
-                        if (2 * s < n_seg) {
-                            v.ws[s][0] = __ldg(ws0 + off / 128 + s);
-                            v.ws[s][1] = __ldg(ws1 + off / 128 + s);
-                        }
-                }
-            };
-            if (!fw_stage<BF16, NT, false, BLOCK, false>(acc, ring, n, bytes, load, ctx, abort_flag)) return fw_settle();
-            fill_next();
-        }
-        const float sc = BF16 ? 1.0f : BLOCK ? a.x_scale : __fmul_rn(a.su[e], a.x_scale);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int row = g + 8 * (c / 2);
-                const int hr = rowi[i * 16 + nt * 8 + 2 * q + c % 2];
-                if (hr == FEW_ABSENT || row >= n) continue;
-                float z = acc[nt][c];
-                if constexpr (!BF16) z = __fmul_rn(z, sc);
-                const float h = z <= 0.0f ? 0.0f : __fmul_rn(z, z);   // a NaN stays one
-                const int64_t o = (int64_t)hr * a.F + f + row;
-                if constexpr (BF16) {
-                    // h as the sum of two bf16, 16 bits of it: one alone would add a second rounding
-                    // of the output's size
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-                    const float top = __bfloat162float(hi);
-                    reinterpret_cast<__nv_bfloat16*>(a.h)[o] = hi;
-                    reinterpret_cast<__nv_bfloat16*>(a.h + a.h_lo)[o] =
-                        __float2bfloat16_rn(top < __uint_as_float(0x7f800000u) ? __fsub_rn(h, top) : 0.0f);
-                } else {
-                    a.h[o] = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(h, a.h_scale), __NV_SATFINITE, __NV_E4M3);
-                }
-            }
+        const int i = piece / per, f = (piece - i * per) * FEW_PIECE;
+        const int n_tok = lst_n[i];
+        const bool ok = n_tok <= 8
+                            ? few_up<FMT, 1>(a, ring, lst_e[i], f, n_tok, rowi + i * 16, tok + i * 16, ctx, abort_flag)
+                            : few_up<FMT, 2>(a, ring, lst_e[i], f, n_tok, rowi + i * 16, tok + i * 16, ctx, abort_flag);
+        if (!ok) return fw_settle();
         __syncwarp();
         if (lane == 0 && !(a.hold && piece == 0)) {
             __threadfence();
@@ -456,65 +600,22 @@ __global__ void __launch_bounds__(FW_THREADS, 1) few_layer_kernel(FewArgs a, Dev
         if (!__shfl_sync(0xffffffffu, good, 0)) return fw_settle();
         __syncwarp();
     }
-    const int kb = a.down.bytes / 128;
     for (int un = 0; un < a.share.units; ++un) {
         const int u = blockIdx.x * a.share.units + un;
-        const int d0 = group_row(u, my_group), n = group_row(u, my_group + 1) - d0;
-        float tot[NT][4] = {};
-        FwPairs pr{0, 0};
-        pr.seek(n_list, a.down.n, wk, gw);
-        while (n > 0 && pr.i < n_list) {
-            const int i = pr.i, e = lst_e[i];
-            FwRows<NT> act;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int r = rowi[i * 16 + nt * 8 + g];
-                act.on[nt] = r != FEW_ABSENT;
-                act.p[nt] = a.h + (int64_t)r * a.F * ES + q * 16;
-            }
-            const float* ws0 = BLOCK ? a.sd + ((int64_t)e * a.H + d0 + min(g, n - 1)) * kb : nullptr;
-            const float* ws1 = BLOCK ? a.sd + ((int64_t)e * a.H + d0 + min(g + 8, n - 1)) * kb : nullptr;
-            float acc[NT][4] = {};
-            for (; pr.i == i; pr.step(n_list, a.down.n, wk, gw)) {
-                const int c0 = pr.k * a.down.chunk, bytes = min(a.down.chunk, a.down.bytes - c0);
-                auto load = [&](auto& v, int seg0, int n_seg) {
-                    const int off = c0 + seg0 * FW_SEG;
-                    fw_load(v, act, off, n_seg, a.F * ES, a.h_lo);
-                    if constexpr (BLOCK) {
-#pragma unroll
-                        for (int s = 0; s < FW_GROUP / 2; ++s)
-                            if (2 * s < n_seg) {
-                                v.ws[s][0] = __ldg(ws0 + off / 128 + s);
-                                v.ws[s][1] = __ldg(ws1 + off / 128 + s);
-                            }
-                    }
-                };
-                if (!fw_stage<BF16, NT, BF16, BLOCK, false>(acc, ring, n, bytes, load, ctx, abort_flag))
-                    return fw_settle();
-                fill_next();
-            }
-            // this warp's part of the expert's output, weighted, for the tokens routed to it only
-            // (another expert's infinity must not reach a token as 0 * inf)
-            const float sc = FMT == MOE_FP8_E4M3 ? a.sd[e] : 1.0f;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int t = i * 16 + nt * 8 + 2 * q + c;
-                    if (rowi[t] == FEW_ABSENT) continue;
-                    const float w = wt[t] * sc;
-                    tot[nt][c] = __fmaf_rn(w, acc[nt][c], tot[nt][c]);
-                    tot[nt][c + 2] = __fmaf_rn(w, acc[nt][c + 2], tot[nt][c + 2]);
-                }
+        const int d0 = unit_row(u), n = unit_row(u + 1) - d0;
+        float* tot = red.mine(warp);
+        for (int j = lane; j < FwRed::kWarp; j += 32) tot[j] = 0.0f;
+        __syncwarp();
+        if (n > 0) {
+            FewDown<FMT> down{a, ring, lst_e, lst_n, rowi, tok, wt, n_list, warp, d0, n, tot, ctx, abort_flag};
+            if (!down.run()) return fw_settle();
         }
-        if (!red.exchange(tot, warp, ctx, abort_flag)) return fw_settle();
-        const int r0 = group_row(u, 0), rows = group_row(u, a.share.groups) - r0;
-        const int half = group_row(u, 1) - r0;   // rows of the first group
-        for (int j = tid; j < rows * a.T; j += FW_THREADS) {
-            const int t = j / rows, row = j - t * rows;
-            float o = row < half ? red.sum(row, t, 0, gw) : red.sum(row - half, t, gw, gw);
-            if constexpr (!BF16) o = __fmul_rn(o, a.h_scale);
-            const int64_t at = (int64_t)t * a.H + r0 + row;
+        if (!red.exchange(ctx, abort_flag)) return fw_settle();
+        for (int j = tid; j < n * a.T; j += 32 * FW_WARPS) {
+            const int t = j / n, row = j - t * n;
+            float o = red.sum(t, row);
+            if constexpr (FMT != MOE_BF16) o = __fmul_rn(o, a.h_scale);
+            const int64_t at = (int64_t)t * a.H + d0 + row;
             if (a.residual) o = __fadd_rn(o, bf16_bits_to_float(a.residual[at]));
             a.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
         }
@@ -525,20 +626,41 @@ __global__ void __launch_bounds__(FW_THREADS, 1) few_layer_kernel(FewArgs a, Dev
 
 static int few_row_bytes(int K, int dtype) { return dtype == MOE_BF16 ? 2 * K : dtype == MOE_FP8_B128 ? (K + 127) / 128 * 128 : K; }
 
-template <int FMT, int NT>
-static cudaError_t launch_layer(FewArgs& a, int num_sms, const DevCtx& ctx, cudaStream_t stream) {
-    const size_t fixed = 2 * FwRed<NT>::kFloats * sizeof(float) + few_table_bytes(a.n_list_max);
-    a.n_stages = (int)std::min<size_t>(FW_MAX_STAGES, (FW_SMEM - fixed) / FW_WARPS / a.slot_bytes);
-    const size_t smem = (size_t)FW_WARPS * a.n_stages * a.slot_bytes + fixed;
-    auto k = few_layer_kernel<FMT, NT>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    return launch_k(k, dim3(num_sms), dim3(FW_THREADS), smem, stream, a, ctx);
+typedef CUresult (*FwEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static FwEncodeFn fw_encode_fn() {
+    static const FwEncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<FwEncodeFn>(p) : nullptr;
+    }();
+    return fn;
+}
+
+bool fw_map(CUtensorMap* m, const void* base, int64_t rows, int64_t bytes, int64_t ld, int chunk, int box_rows) {
+    const FwEncodeFn fn = fw_encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)bytes / 4, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {(cuuint32_t)chunk / 4, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int FMT>
-static cudaError_t launch_fmt(FewArgs& a, int num_sms, const DevCtx& ctx, cudaStream_t stream) {
-    return a.T <= 8 ? launch_layer<FMT, 1>(a, num_sms, ctx, stream) : launch_layer<FMT, 2>(a, num_sms, ctx, stream);
+static cudaError_t launch_layer(const FewMaps& maps, FewArgs& a, int num_sms, const DevCtx& ctx, cudaStream_t stream) {
+    const size_t fixed = FwRed::bytes(a.share.units) + few_table_bytes(a.n_list_max);
+    a.n_stages = (int)std::min<size_t>(FW_MAX_STAGES, (FW_SMEM - fixed) / FW_WARPS / a.slot_bytes);
+    const size_t smem = (size_t)FW_WARPS * a.n_stages * a.slot_bytes + fixed;
+    auto k = few_layer_kernel<FMT>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_k(k, dim3(num_sms), dim3(FW_THREADS), smem, stream, maps, a, ctx);
 }
 
 cudaError_t launch_few(const moe_dims* d, const uint16_t* x, const uint16_t* wr, const float* bias, const void* w_up,
@@ -568,10 +690,6 @@ cudaError_t launch_few(const moe_dims* d, const uint16_t* x, const uint16_t* wr,
     a.topk_w = w;
     a.logits = ws.logits;
     a.act = fp8 ? ws.xq : reinterpret_cast<const uint8_t*>(x);
-    a.w_up = static_cast<const uint8_t*>(w_up);
-    a.w_down = static_cast<const uint8_t*>(w_down);
-    a.w_up_s = static_cast<const uint8_t*>(w_up_s);
-    a.w_down_s = static_cast<const uint8_t*>(w_down_s);
     a.su = fp8 ? sc->w_up_scale : nullptr;
     a.sd = fp8 ? sc->w_down_scale : nullptr;
     a.x_scale = fp8 ? sc->x_scale : 1.0f;
@@ -585,19 +703,28 @@ cudaError_t launch_few(const moe_dims* d, const uint16_t* x, const uint16_t* wr,
     a.E = d->E;
     a.K = d->K;
     a.F = d->F;
-    const int unit = d->expert_dtype == MOE_FP8_B128 ? 128 : FW_SEG;
-    a.up = fw_cut(few_row_bytes(d->H, d->expert_dtype), unit);
-    a.down = fw_cut(few_row_bytes(d->F, d->expert_dtype), unit);
+    const bool block = d->expert_dtype == MOE_FP8_B128;
+    a.up = fw_cut(few_row_bytes(d->H, d->expert_dtype), block);
+    a.down = fw_cut(few_row_bytes(d->F, d->expert_dtype), block);
     a.share = fw_share(d->H, num_sms);
-    a.share.rows = std::max(a.share.rows, 8);   // a narrow output still leaves up pieces of eight rows
-    a.stride = fw_row_stride(std::max(a.up.chunk, a.down.chunk));
-    a.slot_bytes = a.share.rows * a.stride;
+    a.slot_bytes = (std::max(a.share.rows, FEW_PIECE) * a.up.chunk + 127) / 128 * 128;
+    FewMaps maps = {};
+    const int ns = a.ns;
+    bool ok = fw_map(&maps.up, w_up, (int64_t)d->E * d->F, a.up.bytes, a.up.bytes, a.up.chunk, FEW_PIECE);
+    if (ns > 0) ok = ok && fw_map(&maps.up_s, w_up_s, (int64_t)ns * d->F, a.up.bytes, a.up.bytes, a.up.chunk, FEW_PIECE);
+    for (int i = 0; i < 2 && a.share.rows > i; ++i)
+        ok = ok && fw_map(&maps.down[i], w_down, (int64_t)d->E * d->H, a.down.bytes, a.down.bytes, a.down.chunk,
+                          a.share.rows - i);
+    for (int i = 0; i < 2 && ns > 0 && a.share.rows > i; ++i)
+        ok = ok && fw_map(&maps.down_s[i], w_down_s, d->H, (int64_t)d->Fs * 2, (int64_t)d->Fs * 2, a.down.chunk,
+                          a.share.rows - i);
+    if (!ok) return cudaErrorInvalidValue;
     a.n_list_max = (int)std::min<int64_t>(d->E, d->T * d->K) + a.ns;
     a.hold = hold;
     switch (d->expert_dtype) {
-        case MOE_BF16: return launch_fmt<MOE_BF16>(a, num_sms, ctx, stream);
-        case MOE_FP8_E4M3: return launch_fmt<MOE_FP8_E4M3>(a, num_sms, ctx, stream);
-        default: return launch_fmt<MOE_FP8_B128>(a, num_sms, ctx, stream);
+        case MOE_BF16: return launch_layer<MOE_BF16>(maps, a, num_sms, ctx, stream);
+        case MOE_FP8_E4M3: return launch_layer<MOE_FP8_E4M3>(maps, a, num_sms, ctx, stream);
+        default: return launch_layer<MOE_FP8_B128>(maps, a, num_sms, ctx, stream);
     }
 }
 

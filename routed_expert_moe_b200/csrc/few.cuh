@@ -3,21 +3,28 @@
 //
 // A weight row is read once from HBM and meets at most 16 activation rows, so
 // the work is a stream: 2 * 16 operations per weight at most, far below what
-// the tensor cores take at HBM's rate.  Each of a CTA's eight warps runs a
-// pipeline of its own: its lane 0 copies the next rows' chunk of K into the
-// warp's ring in shared memory (one untiled bulk copy per row), the warp waits
-// on that copy's barrier, multiplies with warp-level matrix instructions
-// (weights as the 16-row operand, tokens as the 8-column one), and refills the
-// slot it has read.  No warp waits for another within a stream.  tcgen05 would
-// need 128 weight rows per instruction; here a warp takes 9 or 10, which lets
-// every SM stream the same number of bytes.
+// the tensor cores take at HBM's rate.  Each of a CTA's eight consumer warps
+// has a ring in shared memory of its own.  Lane w of the producer warp fills
+// ring w (one TMA box, 16 to 24 rows of a chunk of K, per stage).  A consumer
+// fetches the activations that go with its next stage into registers, waits
+// for the weights, multiplies with warp-level matrix instructions (tokens as
+// the 16-row operand, weight rows as the 8-column one) and hands the slot
+// back.  No consumer waits for another within a stream.  tcgen05 would need
+// 128 weight rows per instruction; boxes of 16 to 24 rows let every SM stream
+// the same number of bytes.
+//
+// Copying row by row instead (untiled bulk copies) costs a fixed 32 cycles of
+// an SM's copy engine per row: 4.6 TB/s at 512 bytes per row, against 7.0 with
+// boxes.  Consumers that fill their rings themselves spend 500 cycles a stage
+// on it.
 //
 // Lane (g, q) = (lane / 4, lane % 4) of a warp reads 16 bytes at
-// 64 * segment + 16 * q of weight rows g and g + 8 and of token g's
-// activations: the matrix instruction's K index is assigned to those bytes in
-// the same order on both sides, so no value moves between lanes.
+// 64 * segment + 16 * q of weight rows g, g + 8, g + 16 and of tokens g and g + 8:
+// the matrix instruction's K index is assigned to those bytes in the same
+// order on both sides, so no value moves between lanes.
 #pragma once
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -27,47 +34,33 @@
 
 namespace moe {
 
-constexpr int FW_WARPS = 8;
-constexpr int FW_THREADS = 32 * FW_WARPS;
+constexpr int FW_WARPS = 8;                   // consumer warps
+constexpr int FW_THREADS = 32 * (FW_WARPS + 1);
 constexpr int FW_SEG = 64;                    // bytes of a row that one matrix step takes
-constexpr int FW_CHUNK = 768;                 // bytes of a row per stage at most
-constexpr int FW_GROUP = 4;                   // segments whose activations are loaded together
-constexpr int FW_ROWS = 16;                   // weight rows per stage at most
-constexpr int FW_MAX_STAGES = 7;              // of one warp's ring
+constexpr int FW_ROWS = 24;                   // weight rows per stage at most
+constexpr int FW_MAX_STAGES = 6;              // of one warp's ring
 constexpr int FW_SMEM = 227 * 1024;           // shared memory a block may use
 
-// How a weight row of `bytes` bytes is cut into chunks of whole units: segments, or scale blocks.
+// Segments per stage.  Five: an odd number puts the rows of a stage, 320 bytes apart, into
+// alternating halves of the banks.  Formats with a scale per 128 bytes take whole blocks.
+constexpr int fw_segs(bool block) { return block ? 6 : 5; }
+
+// How a weight row of `bytes` bytes is cut into chunks (the last one may reach past the row: zeros).
 struct FwCut {
     int bytes;    // of a row
-    int chunk;    // bytes per stage; the last one may be shorter
+    int chunk;    // bytes per stage
     int n;        // chunks per row
 };
-inline FwCut fw_cut(int bytes, int unit) {
+inline FwCut fw_cut(int bytes, bool block) {
     FwCut c;
     c.bytes = bytes;
-    const int n = (bytes + FW_CHUNK - 1) / FW_CHUNK;
-    c.chunk = ((bytes + n - 1) / n + unit - 1) / unit * unit;
+    c.chunk = fw_segs(block) * FW_SEG;
     c.n = (bytes + c.chunk - 1) / c.chunk;
     return c;
 }
-// Distance between two rows of a stage: 64 bytes modulo 128, so that the two rows that eight
-// neighbouring lanes read lie in different banks.
-inline int fw_row_stride(int chunk) { return chunk % 128 == 64 ? chunk : chunk + 64; }
 
-__device__ __forceinline__ void fw_bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
-                                             uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
-        ::"r"(dst), "l"(src), "r"(bytes), "r"(bar), "l"(policy) : "memory");
-}
-
-__device__ __forceinline__ uint4 fw_lds(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-
-// D (16 x 8, fp32) += A (16 rows x 32 bytes) * B (8 columns x 32 bytes): bf16 or E4M3 operands.
+// D (16 tokens x 8 weight rows, fp32) += A (16 x 32 bytes) * B (8 x 32 bytes): bf16 or E4M3 operands
+// (volatile: it must stay where the whole warp is converged).
 template <bool BF16>
 __device__ __forceinline__ void fw_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
@@ -83,210 +76,290 @@ __device__ __forceinline__ void fw_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One warp's ring.
-struct FwRing {
-    uint32_t base;       // slots
-    uint32_t bars;       // one mbarrier per slot (8 bytes each)
-    int slot_bytes, stride, n;
-    int put, take;       // next slot to fill, to read
-    uint32_t parity;     // of the next slot to read
-    uint64_t policy;
+// The rings' barriers and slots in shared memory, [warp][slot].
+struct FwRings {
+    uint8_t* base;
+    uint64_t* full;      // one arrival (the producer's) and the box's bytes
+    uint64_t* empty;     // one arrival (the consumer's)
+    int slot_bytes, n;
 
-    // Starts the copy of `rows` rows of `bytes` bytes, ld bytes apart.  Whole warp, converged; every
-    // lane has finished reading the slot.
-    __device__ __forceinline__ void fill(const uint8_t* src, int64_t ld, int rows, uint32_t bytes) {
-        if (threadIdx.x % 32 == 0) {
-            const uint32_t bar = bars + 8 * put;
-            uint32_t dst = base + put * slot_bytes;
-            mbar_arrive_expect_tx(bar, bytes * rows);
-            for (int r = 0; r < rows; ++r, dst += stride, src += ld) fw_bulk_load(dst, src, bytes, bar, policy);
+    static constexpr size_t kBarBytes = 2 * FW_WARPS * FW_MAX_STAGES * sizeof(uint64_t);
+    __device__ __forceinline__ void init() const {   // one thread
+        for (int i = 0; i < FW_WARPS * FW_MAX_STAGES; ++i) {
+            mbar_init(smem_u32(full + i), 1);
+            mbar_init(smem_u32(empty + i), 1);
         }
-        if (++put == n) put = 0;
     }
-    // Waits for the next slot; returns its address in `slot`.
-    __device__ __forceinline__ bool wait(uint32_t& slot, const DevCtx& ctx, volatile int* abort) {
-        slot = base + take * slot_bytes;
-        return mbar_wait_warp(bars + 8 * take, parity, ctx, abort);
+};
+
+// Consumer side of ring `warp`.
+struct FwTake {
+    const uint8_t* base;
+    uint32_t full, empty;
+    int slot_bytes, n, slot;
+    uint32_t parity;
+
+    __device__ __forceinline__ FwTake(const FwRings& r, int warp)
+        : base(r.base + (size_t)warp * r.n * r.slot_bytes),
+          full(smem_u32(r.full + warp * FW_MAX_STAGES)),
+          empty(smem_u32(r.empty + warp * FW_MAX_STAGES)),
+          slot_bytes(r.slot_bytes),
+          n(r.n),
+          slot(0),
+          parity(0) {}
+    // Waits for the next slot.  Every lane looks at the barrier, so that data that is there already
+    // costs one look.
+    __device__ __forceinline__ bool wait(const DevCtx& ctx, volatile int* abort) {
+        const uint32_t bar = full + 8 * slot;
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        return mbar_wait_warp(bar, parity, ctx, abort) && __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
     }
-    __device__ __forceinline__ void next() {
-        if (++take == n) {
-            take = 0;
+    __device__ __forceinline__ const uint8_t* data() const { return base + slot * slot_bytes; }
+    // Every lane has read the slot: hands it back.
+    __device__ __forceinline__ void release() {
+        __syncwarp();
+        if (threadIdx.x % 32 == 0) mbar_arrive(empty + 8 * slot);
+        if (++slot == n) {
+            slot = 0;
             parity ^= 1u;
         }
     }
 };
 
-// A lane's activations and block scales for FW_GROUP segments.
-template <int NT, bool SPLIT, bool BLOCK, bool BLOCK_ACT>
-struct FwActs {
-    uint4 b[FW_GROUP][NT];                        // 16 bytes of token g + 8 * nt
-    uint4 lo[SPLIT ? FW_GROUP : 1][NT];           // low parts (SPLIT: an activation is the sum of two bf16)
-    float ws[BLOCK ? FW_GROUP / 2 : 1][2];        // scale of weight rows g, g + 8 per 128-byte block
-    float xs[BLOCK_ACT ? FW_GROUP / 2 : 1][NT][2];   // scale of tokens 8 nt + 2 q, + 1 per block
+// Producer side of one ring: one lane of the producer warp each.
+struct FwPut {
+    uint8_t* base;
+    uint32_t full, empty;
+    int slot_bytes, n, slot;
+    uint32_t parity;
+
+    __device__ __forceinline__ FwPut(const FwRings& r, int warp)
+        : base(r.base + (size_t)warp * r.n * r.slot_bytes),
+          full(smem_u32(r.full + warp * FW_MAX_STAGES)),
+          empty(smem_u32(r.empty + warp * FW_MAX_STAGES)),
+          slot_bytes(r.slot_bytes),
+          n(r.n),
+          slot(0),
+          parity(1) {}
+    __device__ __forceinline__ bool ready() const {   // no wait
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(empty + 8 * slot), "r"(parity)
+            : "memory");
+        return ok != 0;
+    }
+    __device__ __forceinline__ void next() {
+        if (++slot == n) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
+    // Starts the copy of a box of `bytes` bytes at byte x of row y into the next slot.
+    __device__ __forceinline__ void fill(const CUtensorMap* map, int x, int y, uint32_t bytes, uint64_t policy) {
+        const uint32_t bar = full + 8 * slot;
+        mbar_arrive_expect_tx(bar, bytes);
+        tma_load_2d(smem_u32(base) + slot * slot_bytes, map, bar, x / 4, y, policy);
+        next();
+    }
+    // Hands over an empty slot (the consumer looks at what stands beside it).
+    __device__ __forceinline__ void mark() {
+        mbar_arrive(full + 8 * slot);
+        next();
+    }
 };
 
-// A lane's rows of activations: its tokens g + 8 * nt (+ 16 q bytes), zeros for a token that is not there.
-template <int NT>
-struct FwRows {
-    const uint8_t* p[NT];
-    bool on[NT];
-};
-__device__ __forceinline__ uint4 fw_ld16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
-
-// Fetches FW_GROUP segments from byte c0 of the rows on.  `n_seg` of them are in the stage; rows hold
-// `row_bytes` bytes (a row may end inside the last one).  lo: distance to the low parts.
-template <int NT, bool SPLIT, bool BLOCK, bool BLOCK_ACT>
-__device__ __forceinline__ void fw_load(FwActs<NT, SPLIT, BLOCK, BLOCK_ACT>& v, const FwRows<NT>& r, int c0, int n_seg,
-                                        int row_bytes, int64_t lo) {
-    const int q16 = (threadIdx.x % 4) * 16;
-    const bool whole = n_seg >= FW_GROUP && c0 + FW_GROUP * FW_SEG <= row_bytes;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int s = 0; s < FW_GROUP; ++s) {
-            v.b[s][nt] = make_uint4(0, 0, 0, 0);
-            if constexpr (SPLIT) v.lo[s][nt] = make_uint4(0, 0, 0, 0);
+// The producer warp's loop: step() fills one stage of this lane's ring, false once there is none left.
+// A lane looks for a free slot without waiting, so that one slow ring does not hold up the others.
+// Ends (false) when no ring made progress for the time limit or a consumer gave up.
+template <typename Step>
+__device__ __forceinline__ bool fw_produce(FwPut& put, bool active, const Step& step, const DevCtx& ctx,
+                                           volatile int* abort) {
+    uint64_t t0 = globaltimer();
+    uint32_t idle = 0;
+    while (__any_sync(0xffffffffu, active)) {
+        bool moved = false;
+        if (active && put.ready()) {
+            active = step();
+            moved = true;
         }
-        if (r.on[nt]) {
-            if (whole) {
-#pragma unroll
-                for (int s = 0; s < FW_GROUP; ++s) {
-                    v.b[s][nt] = fw_ld16(r.p[nt] + c0 + s * FW_SEG);
-                    if constexpr (SPLIT) v.lo[s][nt] = fw_ld16(r.p[nt] + lo + c0 + s * FW_SEG);
-                }
-            } else {
-#pragma unroll
-                for (int s = 0; s < FW_GROUP; ++s)
-                    if (s < n_seg && c0 + s * FW_SEG + q16 < row_bytes) {
-                        v.b[s][nt] = fw_ld16(r.p[nt] + c0 + s * FW_SEG);
-                        if constexpr (SPLIT) v.lo[s][nt] = fw_ld16(r.p[nt] + lo + c0 + s * FW_SEG);
-                    }
+        if (__any_sync(0xffffffffu, moved)) {
+            idle = 0;
+            continue;
+        }
+        if ((++idle & 63u) == 0) {
+            if (idle == 64) t0 = globaltimer();
+            bool stop = *abort != 0;
+            if (globaltimer() - t0 > ctx.timeout_ns) {
+                record_error(ctx.err, MOE_ETIMEOUT);
+                *abort = 1;
+                stop = true;
             }
+            if (__any_sync(0xffffffffu, stop)) return false;
         }
     }
-}
-
-// One group of segments seg0 .. of a stage: weight rows g and g + 8 at r0 and r1 (this lane's 16
-// bytes of segment 0), `left` bytes of the row remain from the chunk's start.
-template <bool BF16, int NT, bool SPLIT, bool BLOCK, bool BLOCK_ACT>
-__device__ __forceinline__ void fw_group(float (&acc)[NT][4], uint32_t r0, uint32_t r1, int seg0, int n_seg, int left,
-                                         const FwActs<NT, SPLIT, BLOCK, BLOCK_ACT>& v) {
-    const int q16 = (threadIdx.x % 4) * 16;
-#pragma unroll
-    for (int s = 0; s < FW_GROUP; s += 2) {
-        if (seg0 + s >= n_seg) break;
-        float part[NT][4] = {};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int seg = seg0 + s + h;
-            if (seg >= n_seg) break;
-            uint4 a0 = fw_lds(r0 + seg * FW_SEG), a1 = fw_lds(r1 + seg * FW_SEG);
-            if (seg * FW_SEG + FW_SEG > left) {   // the row ends inside the segment
-                if (seg * FW_SEG + q16 >= left) a0 = a1 = make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float(&d)[4] = BLOCK ? part[nt] : acc[nt];
-                const uint4 b = v.b[s + h][nt];
-                fw_mma<BF16>(d, a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-                fw_mma<BF16>(d, a0.z, a1.z, a0.w, a1.w, b.z, b.w);
-                if constexpr (SPLIT) {
-                    const uint4 l = v.lo[s + h][nt];
-                    fw_mma<BF16>(d, a0.x, a1.x, a0.y, a1.y, l.x, l.y);
-                    fw_mma<BF16>(d, a0.z, a1.z, a0.w, a1.w, l.z, l.w);
-                }
-            }
-        }
-        if constexpr (BLOCK) {   // the two segments are one block of 128
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float sc = v.ws[s / 2][c / 2];
-                    if constexpr (BLOCK_ACT) sc *= v.xs[s / 2][nt][c % 2];
-                    acc[nt][c] = __fmaf_rn(sc, part[nt][c], acc[nt][c]);
-                }
-        }
-    }
-}
-
-// One stage: load(v, seg0, n) fetches the activations of a group (n segments of the stage from seg0); the first group's are under way while the
-// warp waits for the weights, the next group's while one is multiplied.
-template <bool BF16, int NT, bool SPLIT, bool BLOCK, bool BLOCK_ACT, typename Load>
-__device__ __forceinline__ bool fw_stage(float (&acc)[NT][4], FwRing& ring, int rows, int bytes, const Load& load,
-                                         const DevCtx& ctx, volatile int* abort) {
-    const int lane = threadIdx.x % 32, g = lane / 4, q16 = (lane % 4) * 16;
-    const int n_seg = (bytes + FW_SEG - 1) / FW_SEG;
-    FwActs<NT, SPLIT, BLOCK, BLOCK_ACT> v0, v1;
-    load(v0, 0, n_seg);
-    uint32_t slot;
-    if (!ring.wait(slot, ctx, abort)) return false;
-    // rows past the tile repeat its last one: their products are not used
-    const uint32_t r0 = slot + min(g, rows - 1) * ring.stride + q16, r1 = slot + min(g + 8, rows - 1) * ring.stride + q16;
-#pragma unroll
-    for (int s = 0; s < FW_CHUNK / FW_SEG; s += 2 * FW_GROUP) {
-        if (s + FW_GROUP < n_seg) load(v1, s + FW_GROUP, n_seg - s - FW_GROUP);
-        fw_group<BF16, NT, SPLIT, BLOCK, BLOCK_ACT>(acc, r0, r1, s, n_seg, bytes, v0);
-        if (s + 2 * FW_GROUP < n_seg) load(v0, s + 2 * FW_GROUP, n_seg - s - 2 * FW_GROUP);
-        if (s + FW_GROUP < n_seg)
-            fw_group<BF16, NT, SPLIT, BLOCK, BLOCK_ACT>(acc, r0, r1, s + FW_GROUP, n_seg, bytes, v1);
-    }
-    ring.next();
-    __syncwarp();   // every lane has read the slot: the caller may fill it again
     return true;
 }
 
-// The pairs (expert i, chunk k) of a stream of n_list x n_chunks that fall to warp w of n_w (a power
-// of two).  The chunks rotate over the warps from one expert to the next, so that a short last chunk
-// does not always fall to the same warp.
+// What goes with the weights of one stage, in registers: 16 bytes per segment of the two activation
+// rows that this lane supplies (rows g and g + 8 of the 16-row operand; TWO: they differ), and the
+// scales of its results.  Fetched while the warp still waits for the weights, or fills its ring.
+template <int NT, bool TWO, bool BLOCK, bool BLOCK_ACT>
+struct FwActs {
+    static constexpr int SEGS = fw_segs(BLOCK), KB = BLOCK ? SEGS / 2 : 1;
+    uint4 x[SEGS][TWO ? 2 : 1];
+    float ws[KB][BLOCK ? NT : 1][2];               // weight rows 8 nt + 2 q, + 1
+    float xs[BLOCK_ACT ? KB : 1][TWO ? 2 : 1];     // activation rows g, g + 8
+};
+
+// Where they come from: from the start of a K row on, this lane's + 16 q bytes.  A token slot without a
+// token, like a row past the tile, repeats another one and is not used.
+template <int NT>
+struct FwSide {
+    const uint8_t* act[2];
+    const float* ws[NT][2];
+    const float* xs[2];
+};
+
+// Bytes c0 .. of the rows, which hold row_bytes (zeros past them; weights may be padded).
+template <int NT, bool TWO, bool BLOCK, bool BLOCK_ACT>
+__device__ __forceinline__ void fw_fetch(FwActs<NT, TWO, BLOCK, BLOCK_ACT>& v, const FwSide<NT>& side, int c0,
+                                         int row_bytes) {
+    using A = FwActs<NT, TWO, BLOCK, BLOCK_ACT>;
+    const int q16 = (threadIdx.x % 4) * 16;
+    const bool full = c0 + A::SEGS * FW_SEG <= row_bytes;
+#pragma unroll
+    for (int t = 0; t < (TWO ? 2 : 1); ++t) {
+        const uint8_t* p = side.act[t] + c0;
+        if (full) {
+#pragma unroll
+            for (int s = 0; s < A::SEGS; ++s) v.x[s][t] = *reinterpret_cast<const uint4*>(p + s * FW_SEG);
+        } else {
+#pragma unroll
+            for (int s = 0; s < A::SEGS; ++s) {
+                v.x[s][t] = make_uint4(0, 0, 0, 0);
+                if (c0 + s * FW_SEG + q16 < row_bytes) v.x[s][t] = *reinterpret_cast<const uint4*>(p + s * FW_SEG);
+            }
+        }
+    }
+    if constexpr (BLOCK) {
+#pragma unroll
+        for (int b = 0; b < A::KB; ++b) {
+            const bool in = full || c0 + b * 128 < row_bytes;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) v.ws[b][nt][j] = in ? __ldg(side.ws[nt][j] + c0 / 128 + b) : 0.0f;
+            if constexpr (BLOCK_ACT) {
+#pragma unroll
+                for (int t = 0; t < (TWO ? 2 : 1); ++t) v.xs[b][t] = in ? __ldg(side.xs[t] + c0 / 128 + b) : 0.0f;
+            }
+        }
+    }
+}
+
+// The running sums of 16 activation rows x 8 NT weight rows, in two chains that do not wait for one
+// another.  j: activation row g (+ 8 * (j / 2)), weight row 8 nt + 2 q + j % 2.
+template <int NT>
+struct FwAcc {
+    float d[2][NT][4];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[0][nt][j] = d[1][nt][j] = 0.0f;
+    }
+    __device__ __forceinline__ float sum(int nt, int j) const { return d[0][nt][j] + d[1][nt][j]; }
+};
+
+// One stage: `rows` weight rows (at most 8 NT) in the slot, times the activations. (tiles of
+// eight past them are skipped).
+template <bool BF16, int NT, bool TWO, bool BLOCK, bool BLOCK_ACT>
+__device__ __forceinline__ void fw_mul(FwAcc<NT>& acc, const uint8_t* slot, int rows,
+                                       const FwActs<NT, TWO, BLOCK, BLOCK_ACT>& v) {
+    constexpr int SEGS = fw_segs(BLOCK);
+    const int lane = threadIdx.x % 32, g = lane / 4, q16 = (lane % 4) * 16;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        if (nt * 8 >= rows) break;
+        // rows past the last repeat it: their results are not used
+        const uint8_t* r = slot + min(nt * 8 + g, rows - 1) * (SEGS * FW_SEG) + q16;
+        float part[2][4];
+#pragma unroll
+        for (int s = 0; s < SEGS; ++s) {
+            const uint4 a = v.x[s][0], b = v.x[s][TWO ? 1 : 0], w = *reinterpret_cast<const uint4*>(r + s * FW_SEG);
+            if constexpr (BLOCK) {
+                if (s % 2 == 0) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) part[0][j] = part[1][j] = 0.0f;
+                }
+                fw_mma<BF16>(part[0], a.x, b.x, a.y, b.y, w.x, w.y);
+                fw_mma<BF16>(part[1], a.z, b.z, a.w, b.w, w.z, w.w);
+                if (s % 2 == 1) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float sc = v.ws[s / 2][nt][j % 2];
+                        if constexpr (BLOCK_ACT) sc *= v.xs[s / 2][TWO ? j / 2 : 0];
+                        float& d = acc.d[s / 2 % 2][nt][j];
+                        d = __fmaf_rn(sc, part[0][j] + part[1][j], d);
+                    }
+                }
+            } else {
+                fw_mma<BF16>(acc.d[0][nt], a.x, b.x, a.y, b.y, w.x, w.y);
+                fw_mma<BF16>(acc.d[1][nt], a.z, b.z, a.w, b.w, w.z, w.w);
+            }
+        }
+    }
+}
+
+// The pairs (list entry i, chunk k) of a stream that fall to warp w.  The chunks rotate over the warps
+// from one expert to the next, so that a short last chunk does not always fall to the same warp; the
+// rotation goes by the expert's number, so that a token's sums do not hang on the experts that others
+// brought into the list.
 struct FwPairs {
     int i, k;
-    __device__ __forceinline__ void seek(int n_list, int n_chunks, int w, int n_w) {   // from expert i's first
+    __device__ __forceinline__ void seek(const int* list, int n_list, int n_chunks, int w) {
         for (; i < n_list; ++i) {
-            k = (w - i * (n_chunks | 1)) & (n_w - 1);
+            k = (w - list[i] * (n_chunks | 1)) & (FW_WARPS - 1);
             if (k < n_chunks) return;
         }
     }
-    __device__ __forceinline__ void step(int n_list, int n_chunks, int w, int n_w) {
-        k += n_w;
+    __device__ __forceinline__ void step(const int* list, int n_list, int n_chunks, int w) {
+        k += FW_WARPS;
         if (k < n_chunks) return;
         ++i;
-        seek(n_list, n_chunks, w, n_w);
+        seek(list, n_list, n_chunks, w);
     }
 };
 
-// The warps' partial sums of one tile, [warp][row][token].  Two buffers take turns, so that one
-// barrier per tile (bounded: every warp arrives, then waits for all eight) orders both the reads after
-// the writes and the next writes after the reads.
-template <int NT>
+// The warps' partial sums of one unit, [warp][token][row], and their exchange.  Two buffers take
+// turns (one is enough for a single unit), so that one barrier per unit (bounded: every warp arrives,
+// then waits for all) orders both the reads after the writes and the next unit's writes after the reads.
 struct FwRed {
-    static constexpr int kWarp = FW_ROWS * NT * 8;
+    static constexpr int kWarp = 16 * FW_ROWS;
     static constexpr int kFloats = FW_WARPS * kWarp;
-    float* buf;          // [2][kFloats]
+    static constexpr size_t bytes(int units) { return (units > 1 ? 2 : 1) * kFloats * sizeof(float); }
+    float* buf;          // [2][kFloats], or [1] for a single unit
     uint32_t bar;        // mbarrier of FW_WARPS arrivals
     int turn;
 
-    __device__ __forceinline__ bool exchange(const float (&acc)[NT][4], int warp, const DevCtx& ctx,
-                                             volatile int* abort) {
-        const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
-        float* b = buf + (turn & 1) * kFloats + warp * kWarp;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float* p = b + g * NT * 8 + nt * 8 + 2 * q;
-            *reinterpret_cast<float2*>(p) = make_float2(acc[nt][0], acc[nt][1]);
-            *reinterpret_cast<float2*>(p + 8 * NT * 8) = make_float2(acc[nt][2], acc[nt][3]);
-        }
+    __device__ __forceinline__ float* mine(int warp) const { return buf + (turn & 1) * kFloats + warp * kWarp; }
+    __device__ __forceinline__ bool exchange(const DevCtx& ctx, volatile int* abort) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
+        if (threadIdx.x % 32 == 0) mbar_arrive(bar);
         const bool ok = mbar_wait_warp(bar, turn & 1, ctx, abort);
         ++turn;
         return ok;
     }
-    // after exchange(): element (row, token) over warps w0 .. w0 + n_w, in order
-    __device__ __forceinline__ float sum(int row, int token, int w0, int n_w) const {
-        const float* b = buf + ((turn & 1) ^ 1) * kFloats + w0 * kWarp + row * NT * 8 + token;
+    // after exchange(): element (token, row) over the warps, in order
+    __device__ __forceinline__ float sum(int token, int row) const {
+        const float* b = buf + ((turn & 1) ^ 1) * kFloats + token * FW_ROWS + row;
         float s = 0.0f;
-        for (int w = 0; w < n_w; ++w) s += b[w * kWarp];
+#pragma unroll
+        for (int w = 0; w < FW_WARPS; ++w) s += b[w * kWarp];
         return s;
     }
 };
@@ -297,21 +370,22 @@ __device__ __forceinline__ void fw_settle() {
     while (globaltimer() - t0 < 200000ull) __nanosleep(1000);
 }
 
-// A unit of output rows is shared by the CTA's warps: one group of eight warps that split K (up to 16
-// rows) or two groups of four.
+// How n output rows are shared: units of `rows` or `rows` - 1 rows, so many per CTA; a unit's warps
+// split K.
 struct FwShare {
     int units;     // per CTA
-    int groups;    // 1 or 2
-    int rows;      // per group at most
+    int rows;      // per unit at most
 };
 inline FwShare fw_share(int n, int num_sms) {
     FwShare s;
     const int share = (n + num_sms - 1) / num_sms;
-    s.units = (share + 2 * FW_ROWS - 1) / (2 * FW_ROWS);
-    const int per = (share + s.units - 1) / s.units;
-    s.groups = per > FW_ROWS ? 2 : 1;
-    s.rows = (per + s.groups - 1) / s.groups;
+    s.units = (share + FW_ROWS - 1) / FW_ROWS;
+    s.rows = (share + s.units - 1) / s.units;
     return s;
 }
+
+// Map of a row-major matrix of rows of `bytes` bytes, `ld` bytes apart, box `chunk` bytes x box_rows
+// rows (no swizzle; 4-byte elements, so that a box row may hold up to 1 KB).
+bool fw_map(CUtensorMap* m, const void* base, int64_t rows, int64_t bytes, int64_t ld, int chunk, int box_rows);
 
 }  // namespace moe

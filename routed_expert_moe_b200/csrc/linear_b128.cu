@@ -45,109 +45,110 @@ struct LinearFewArgs {
     LinearArgs l;
     FwCut cut;
     FwShare share;
-    int stride, slot_bytes, n_stages;
+    int slot_bytes, n_stages;
 };
 
-template <int NT>
-__global__ void __launch_bounds__(FW_THREADS, 1) linear_few_kernel(LinearFewArgs a, DevCtx ctx) {
+struct LinearFewMaps {
+    CUtensorMap w[2];   // boxes of share.rows weight rows, and of one less
+};
+
+template <int TT>
+__global__ void __launch_bounds__(FW_THREADS, 1)
+    linear_few_kernel(const __grid_constant__ LinearFewMaps maps, LinearFewArgs a, DevCtx ctx) {
     extern __shared__ __align__(1024) uint8_t lf_smem[];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    FwRed<NT> red;
+    FwRed red;
     red.buf = reinterpret_cast<float*>(lf_smem + (size_t)FW_WARPS * a.n_stages * a.slot_bytes);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(red.buf + 2 * FwRed<NT>::kFloats);
-    uint64_t* rbar = bars + FW_WARPS * FW_MAX_STAGES;
+    FwRings rings;
+    rings.base = lf_smem;
+    rings.full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(red.buf) + FwRed::bytes(a.share.units));
+    rings.empty = rings.full + FW_WARPS * FW_MAX_STAGES;
+    rings.slot_bytes = a.slot_bytes;
+    rings.n = a.n_stages;
+    uint64_t* rbar = rings.full + FwRings::kBarBytes / 8;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(rbar + 1);
     red.bar = smem_u32(rbar);
     red.turn = 0;
-    FwRing ring;
-    ring.base = smem_u32(lf_smem) + warp * a.n_stages * a.slot_bytes;
-    ring.bars = smem_u32(bars + warp * FW_MAX_STAGES);
-    ring.slot_bytes = a.slot_bytes;
-    ring.stride = a.stride;
-    ring.n = a.n_stages;
-    ring.put = ring.take = 0;
-    ring.parity = 0;
-    ring.policy = l2_policy_evict_first();
-    if (lane == 0)
-        for (int s = 0; s < a.n_stages; ++s) mbar_init(ring.bars + 8 * s, 1);
     if (tid == 0) {
+        rings.init();
         mbar_init(smem_u32(rbar), FW_WARPS);
         *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&maps.w[0]);
     }
-    if (lane == 0) fence_mbar_init();
     __syncthreads();
     pdl_enter();
 
     const LinearArgs& l = a.l;
-    const int n_groups = gridDim.x * a.share.units * a.share.groups;
-    const int my_group = warp * a.share.groups / FW_WARPS, gw = FW_WARPS / a.share.groups, wk = warp % gw;
-    auto group_row = [&](int u, int grp) { return (int)((int64_t)(u * a.share.groups + grp) * l.N / n_groups); };
-    int f_unit = -1, f_k = 0, f_n0 = 0, f_n = 0;   // the next stage to fill: chunks wk, wk + gw, .. of each unit
-    auto next_unit = [&]() {
-        ++f_unit;
-        f_k = wk;
-        const int u = blockIdx.x * a.share.units + f_unit;
-        f_n0 = group_row(u, my_group);
-        f_n = group_row(u, my_group + 1) - f_n0;
-    };
-    next_unit();
-    auto fill_next = [&]() {
-        while (f_unit < a.share.units) {
-            if (f_k < a.cut.n && f_n > 0) {
-                ring.fill(l.wq + (int64_t)f_n0 * l.Kp + f_k * a.cut.chunk, l.Kp, f_n,
-                          (uint32_t)min(a.cut.chunk, l.Kp - f_k * a.cut.chunk));
-                f_k += gw;
-                return;
-            }
-            next_unit();
-        }
-    };
-    for (int s = 0; s < a.n_stages; ++s) fill_next();
+    const int n_units = gridDim.x * a.share.units;
+    auto unit_row = [&](int u) { return (int)((int64_t)u * l.N / n_units); };
+    if (warp == FW_WARPS) {   // producer: lane w fills ring w, every eighth chunk of each unit
+        const uint64_t policy = l2_policy_evict_first();
+        const int w = lane % FW_WARPS;
+        FwPut put(rings, w);
+        int unit = -1, k = 0, n0 = 0, n = 0;
+        auto next_unit = [&]() {
+            k = w;
+            do {
+                if (++unit == a.share.units || k >= a.cut.n) return false;
+                const int u = blockIdx.x * a.share.units + unit;
+                n0 = unit_row(u);
+                n = unit_row(u + 1) - n0;
+            } while (n <= 0);
+            return true;
+        };
+        const bool active = lane < FW_WARPS && next_unit();
+        auto step = [&]() {
+            put.fill(&maps.w[a.share.rows - n], k * a.cut.chunk, n0, n * a.cut.chunk, policy);
+            k += FW_WARPS;
+            return k < a.cut.n || next_unit();
+        };
+        if (!fw_produce(put, active, step, ctx, abort_flag)) fw_settle();
+        return;
+    }
 
+    FwTake ring(rings, warp);
     const int g = lane / 4, q = lane % 4;
     const int M = (int)l.M;
-    FwRows<NT> act;
-    const float* xs[NT][2];   // scale rows of this lane's result columns
+    FwSide<3> side;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        act.on[nt] = nt * 8 + g < M;
-        act.p[nt] = l.xq + (int64_t)(nt * 8 + g) * l.Kp + q * 16;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) xs[nt][c] = nt * 8 + 2 * q + c < M ? l.xs + (int64_t)(nt * 8 + 2 * q + c) * l.kb : nullptr;
+    for (int t = 0; t < TT; ++t) {
+        const int row = min(t * 8 + g, M - 1);
+        side.act[t] = l.xq + (int64_t)row * l.Kp + q * 16;
+        side.xs[t] = l.xs + (int64_t)row * l.kb;
     }
     for (int un = 0; un < a.share.units; ++un) {
         const int u = blockIdx.x * a.share.units + un;
-        const int n0 = group_row(u, my_group), n = group_row(u, my_group + 1) - n0;
-        const float* ws0 = l.ws + (int64_t)(n0 + min(g, max(n, 1) - 1)) * l.kb;
-        const float* ws1 = l.ws + (int64_t)(n0 + min(g + 8, max(n, 1) - 1)) * l.kb;
-        float acc[NT][4] = {};
-        for (int k = wk; k < a.cut.n && n > 0; k += gw) {
-            const int c0 = k * a.cut.chunk, bytes = min(a.cut.chunk, l.Kp - c0);
-            auto load = [&](auto& v, int seg0, int n_seg) {
-                const int off = c0 + seg0 * FW_SEG;
-                fw_load(v, act, off, n_seg, l.Kp, 0);
+        const int n0 = unit_row(u), n = unit_row(u + 1) - n0;
+        FwAcc<3> acc;
+        acc.clear();
+        if (n > 0 && warp < a.cut.n) {
 #pragma unroll
-                for (int s = 0; s < FW_GROUP / 2; ++s)
-                    if (2 * s < n_seg) {
-                        v.ws[s][0] = __ldg(ws0 + off / 128 + s);
-                        v.ws[s][1] = __ldg(ws1 + off / 128 + s);
+            for (int nt = 0; nt < 3; ++nt)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int c = 0; c < 2; ++c)
-                                v.xs[s][nt][c] = xs[nt][c] ? __ldg(xs[nt][c] + off / 128 + s) : 0.0f;
-                    }
-            };
-            if (!fw_stage<false, NT, false, true, true>(acc, ring, n, bytes, load, ctx, abort_flag)) return fw_settle();
-            fill_next();
+                for (int j = 0; j < 2; ++j) side.ws[nt][j] = l.ws + (int64_t)(n0 + min(nt * 8 + 2 * q + j, n - 1)) * l.kb;
+            FwActs<3, TT == 2, true, true> v;
+            fw_fetch(v, side, warp * a.cut.chunk, l.Kp);
+            for (int k = warp; k < a.cut.n;) {
+                if (!ring.wait(ctx, abort_flag)) return fw_settle();
+                fw_mul<false>(acc, ring.data(), n, v);
+                ring.release();
+                k += FW_WARPS;
+                if (k < a.cut.n) fw_fetch(v, side, k * a.cut.chunk, l.Kp);
+            }
         }
-        if (!red.exchange(acc, warp, ctx, abort_flag)) return fw_settle();
-        const int r0 = group_row(u, 0), rows = group_row(u, a.share.groups) - r0;
-        const int half = group_row(u, 1) - r0;   // rows of the first group
-        for (int j = tid; j < rows * M; j += FW_THREADS) {
-            const int t = j / rows, row = j - t * rows;
-            const float z = row < half ? red.sum(row, t, 0, gw) : red.sum(row - half, t, gw, gw);
-            l.out[(int64_t)t * l.N + r0 + row] = __bfloat16_as_ushort(__float2bfloat16_rn(lin_act(z, l.relu2)));
+        float* mine = red.mine(warp);
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int nt = 0; nt < 3; ++nt)
+                *reinterpret_cast<float2*>(mine + (t * 8 + g) * FW_ROWS + nt * 8 + 2 * q) =
+                    make_float2(acc.sum(nt, 2 * t), acc.sum(nt, 2 * t + 1));
+        if (!red.exchange(ctx, abort_flag)) return fw_settle();
+        for (int j = tid; j < n * M; j += 32 * FW_WARPS) {
+            const int t = j / n, row = j - t * n;
+            const float z = red.sum(t, row);
+            l.out[(int64_t)t * l.N + n0 + row] = __bfloat16_as_ushort(__float2bfloat16_rn(lin_act(z, l.relu2)));
         }
     }
 }
@@ -447,15 +448,18 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
 
 // ----------------------------------------------------------------------------- host
 
-template <int NT>
+template <int TT>
 static cudaError_t launch_linear_few(LinearFewArgs& a, int num_sms, const DevCtx& ctx, cudaStream_t stream) {
-    const size_t fixed = 2 * FwRed<NT>::kFloats * sizeof(float) + (FW_WARPS * FW_MAX_STAGES + 1) * 8 + 16;
+    LinearFewMaps maps = {};
+    for (int i = 0; i < 2 && a.share.rows > i; ++i)
+        if (!fw_map(&maps.w[i], a.l.wq, a.l.N, a.l.Kp, a.l.Kp, a.cut.chunk, a.share.rows - i)) return cudaErrorInvalidValue;
+    const size_t fixed = FwRed::bytes(a.share.units) + FwRings::kBarBytes + 8 + 16;
     a.n_stages = (int)std::min<size_t>(FW_MAX_STAGES, (FW_SMEM - fixed) / FW_WARPS / a.slot_bytes);
     const size_t smem = (size_t)FW_WARPS * a.n_stages * a.slot_bytes + fixed;
-    auto k = linear_few_kernel<NT>;
+    auto k = linear_few_kernel<TT>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_k(k, dim3(num_sms), dim3(FW_THREADS), smem, stream, a, ctx);
+    return launch_k(k, dim3(num_sms), dim3(FW_THREADS), smem, stream, maps, a, ctx);
 }
 
 template <int BN>
@@ -482,10 +486,9 @@ static cudaError_t launch_linear(const LinearArgs& l, int num_sms, const DevCtx&
     if (l.M <= kFewMaxTokens) {
         LinearFewArgs a = {};
         a.l = l;
-        a.cut = fw_cut(l.Kp, 128);
+        a.cut = fw_cut(l.Kp, true);
         a.share = fw_share(l.N, num_sms);
-        a.stride = fw_row_stride(a.cut.chunk);
-        a.slot_bytes = a.share.rows * a.stride;
+        a.slot_bytes = (a.share.rows * a.cut.chunk + 127) / 128 * 128;
         return l.M <= 8 ? launch_linear_few<1>(a, num_sms, ctx, stream) : launch_linear_few<2>(a, num_sms, ctx, stream);
     }
     // the widest tile that still gives every SM one
