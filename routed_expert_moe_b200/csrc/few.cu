@@ -9,7 +9,7 @@
 //
 // 1. few_router_kernel: one block per expert computes its exact logits for all tokens (few enough
 //    tokens that the exact sum costs less than an approximate one with a bound and a second pass);
-//    further blocks write the E4M3 codes of x.  It zeroes the second kernel's counters.
+//    further blocks quantise x.  It zeroes the second kernel's counters.
 // 2. few_layer_kernel, persistent, one CTA of eight warps per SM: every CTA ranks the logits itself
 //    (the same integers give the same choice everywhere), lists the touched experts, and then its
 //    consumer warps stream weights (few.cuh): up pieces (16 rows of one expert, claimed for single warps),
@@ -26,6 +26,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "few.cuh"
@@ -42,10 +43,18 @@ struct FewRouterArgs {
     const float* bias;
     int T, H, E;
     long long* logits;   // [T][E], units of 2^-40
-    uint8_t* xq;         // E4M3 codes of x [T][H], or null
+    __half* xq;          // values of x's E4M3 codes [T][H], or null
     float x_scale;
     int* counters;       // [2]: piece claims, piece reports
 };
+
+// The E4M3 codes (nearest-even, saturating) of two quotients, as a pair of fp16 values.
+__device__ __forceinline__ uint32_t few_code_values(float a, float b) {
+    const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    uint32_t lo, hi;
+    fw_half4(c, lo, hi);
+    return lo;
+}
 
 __global__ void __launch_bounds__(FEW_RT) few_router_kernel(FewRouterArgs a, DevCtx ctx) {
     pdl_enter();
@@ -53,20 +62,18 @@ __global__ void __launch_bounds__(FEW_RT) few_router_kernel(FewRouterArgs a, Dev
     __shared__ float s_x[kFewMaxTokens][8], s_w[8];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int nv = a.H / 8;
-    if ((int)blockIdx.x >= a.E) {   // E4M3 codes of one token
+    if ((int)blockIdx.x >= a.E) {   // one token's E4M3 codes, as values
         const int t = blockIdx.x - a.E;
         const uint4* xr = reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.H);
         for (int v = tid; v < nv; v += FEW_RT) {
             const uint4 p = xr[v];
             const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-            uint32_t c[2] = {0, 0};
+            uint32_t c[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float f = __uint_as_float((j & 1) ? (w[j / 2] & 0xFFFF0000u) : (w[j / 2] << 16));
-                c[j / 4] |= (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(f, a.x_scale), __NV_SATFINITE, __NV_E4M3)
-                            << (8 * (j % 4));
-            }
-            reinterpret_cast<uint2*>(a.xq + (int64_t)t * a.H)[v] = make_uint2(c[0], c[1]);
+            for (int j = 0; j < 4; ++j)
+                c[j] = few_code_values(__fdiv_rn(__uint_as_float(w[j] << 16), a.x_scale),
+                                       __fdiv_rn(__uint_as_float(w[j] & 0xFFFF0000u), a.x_scale));
+            reinterpret_cast<uint4*>(a.xq + (int64_t)t * a.H)[v] = make_uint4(c[0], c[1], c[2], c[3]);
         }
         return;
     }
@@ -133,11 +140,11 @@ struct FewArgs {
     int32_t* topk_idx;          // or null
     float* topk_w;              // or null
     const long long* logits;
-    const uint8_t* act;         // up operand rows: x, or its E4M3 codes
+    const uint8_t* act;         // up operand rows [T][H]: x, or the fp16 values of its E4M3 codes
     const float* su;            // E4M3: [E]; B128: [E][F][kbu]
     const float* sd;            // E4M3: [E]; B128: [E][H][kbd]
     float x_scale, h_scale;
-    uint8_t* h;                 // bf16: high parts [rows][F] then low parts; else codes [rows][F]
+    uint8_t* h;                 // [rows][F]: bf16 high parts and then low parts, or fp16 values of E4M3 codes
     int64_t h_lo;               // bf16: bytes from a high part to its low part
     int* counters;
     int T, H, E, K, F, ns;
@@ -145,6 +152,7 @@ struct FewArgs {
     FwShare share;              // of the output rows
     int slot_bytes, n_stages;
     int n_list_max;
+    int first;                  // pieces that a CTA claims at the start
     int hold;                   // test hook: up piece 0 never reports
 };
 
@@ -210,33 +218,31 @@ __device__ __forceinline__ void few_select(const long long* row, int E, int K, i
     my_w = ex / z;
 }
 
+template <int FMT>
+using FewFmt = FwFmt<FMT == MOE_BF16, false, FMT == MOE_FP8_B128, false>;
+
 // One up piece: 16 rows of a list entry with at most 8 TT tokens.
 template <int FMT, int TT>
 __device__ __forceinline__ bool few_up(const FewArgs& a, FwTake& ring, int e, int f, int n_tok, const uint16_t* rowi,
                                        const uint8_t* tok, const DevCtx& ctx, volatile int* abort) {
-    constexpr bool BF16 = FMT == MOE_BF16, BLOCK = FMT == MOE_FP8_B128;
-    constexpr int ES = BF16 ? 2 : 1;
+    using F = FewFmt<FMT>;
+    constexpr bool BF16 = F::BF16, BLOCK = F::BLOCK;
     const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
-    FwSide<2> side;
+    const int row_bytes = BF16 ? 2 * a.H : a.H;
+    FwSide side;
 #pragma unroll
-    for (int t = 0; t < TT; ++t) side.act[t] = a.act + (int64_t)tok[min(t * 8 + g, n_tok - 1)] * a.H * ES + q * 16;
-    if constexpr (BLOCK) {
-        const int kb = a.up.bytes / 128;
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) side.ws[nt][j] = a.su + ((int64_t)e * a.F + f + nt * 8 + 2 * q + j) * kb;
-    }
+    for (int t = 0; t < TT; ++t) side.act[t] = a.act + (int64_t)tok[min(t * 8 + g, n_tok - 1)] * a.H * 2 + q * F::AB;
+    if constexpr (BLOCK) side.ws = a.su + ((int64_t)e * a.F + f + lane % FEW_PIECE) * (a.up.bytes / 128);
     FwAcc<2> acc;
     acc.clear();
-    FwActs<2, TT == 2, BLOCK, false> v;
-    fw_fetch(v, side, 0, a.H * ES);
+    FwActs<F, fw_batch<F, TT == 2>(), TT == 2> v;
+    fw_fetch(v, side, 0, row_bytes);
     for (int c0 = 0; c0 < a.up.bytes;) {
         if (!ring.wait(ctx, abort)) return false;
-        fw_mul<BF16>(acc, ring.data(), FEW_PIECE, v);
+        fw_mul_stage<F, TT == 2>(acc, ring.data(), FEW_PIECE, c0, row_bytes, side, v);
         ring.release();
         c0 += a.up.chunk;
-        if (c0 < a.up.bytes) fw_fetch(v, side, c0, a.H * ES);
+        if (c0 < a.up.bytes) fw_fetch(v, side, c0, row_bytes);
     }
     const float sc = BF16 ? 1.0f : BLOCK ? a.x_scale : __fmul_rn(a.su[e], a.x_scale);
 #pragma unroll
@@ -261,9 +267,8 @@ __device__ __forceinline__ bool few_up(const FewArgs& a, FwTake& ring, int e, in
                 *reinterpret_cast<__nv_bfloat162*>(a.h + a.h_lo + 2 * o) =
                     __floats2bfloat162_rn(t0 < inf ? __fsub_rn(h[0], t0) : 0.0f, t1 < inf ? __fsub_rn(h[1], t1) : 0.0f);
             } else {
-                const uint32_t c0 = __nv_cvt_float_to_fp8(__fdiv_rn(h[0], a.h_scale), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t c1 = __nv_cvt_float_to_fp8(__fdiv_rn(h[1], a.h_scale), __NV_SATFINITE, __NV_E4M3);
-                *reinterpret_cast<uint16_t*>(a.h + o) = (uint16_t)(c0 | (c1 << 8));
+                *reinterpret_cast<uint32_t*>(a.h + 2 * o) =
+                    few_code_values(__fdiv_rn(h[0], a.h_scale), __fdiv_rn(h[1], a.h_scale));
             }
         }
     }
@@ -274,8 +279,8 @@ __device__ __forceinline__ bool few_up(const FewArgs& a, FwTake& ring, int e, in
 // tot [token][row] (shared memory, this warp's).
 template <int FMT>
 struct FewDown {
-    static constexpr bool BF16 = FMT == MOE_BF16, BLOCK = FMT == MOE_FP8_B128;
-    static constexpr int ES = BF16 ? 2 : 1;
+    using F = FewFmt<FMT>;
+    static constexpr bool BF16 = F::BF16, BLOCK = F::BLOCK;
     const FewArgs& a;
     FwTake& ring;
     const int *lst_e, *lst_n;
@@ -289,20 +294,13 @@ struct FewDown {
 
     // Entry i: activation rows (lo: bf16 low parts), weight scales
     template <int TT>
-    __device__ __forceinline__ void point(FwSide<3>& side, int i, int64_t lo) const {
+    __device__ __forceinline__ void point(FwSide& side, int i, int64_t lo) const {
         const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
         const int last = lst_n[i] - 1;
-        side.act[0] = a.h + (int64_t)rowi[i * 16 + min(g, last)] * a.F * ES + q * 16 + lo;
-        if constexpr (TT == 2) side.act[1] = a.h + (int64_t)rowi[i * 16 + min(8 + g, last)] * a.F * ES + q * 16 + lo;
+        side.act[0] = a.h + (int64_t)rowi[i * 16 + min(g, last)] * a.F * 2 + q * F::AB + lo;
+        if constexpr (TT == 2) side.act[1] = a.h + (int64_t)rowi[i * 16 + min(8 + g, last)] * a.F * 2 + q * F::AB + lo;
         else if constexpr (BF16) side.act[1] = side.act[0] + a.h_lo;   // the low parts are rows 8 .. 15
-        if constexpr (BLOCK) {
-            const int kb = a.down.bytes / 128;
-#pragma unroll
-            for (int nt = 0; nt < 3; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    side.ws[nt][j] = a.sd + ((int64_t)lst_e[i] * a.H + d0 + min(nt * 8 + 2 * q + j, n - 1)) * kb;
-        }
+        if constexpr (BLOCK) side.ws = a.sd + ((int64_t)lst_e[i] * a.H + d0 + min(lane, n - 1)) * (a.down.bytes / 128);
     }
     // Weighted sums of entry i, for the tokens routed to it only
     template <int TT>
@@ -332,20 +330,21 @@ struct FewDown {
     }
     // An entry with more than eight tokens
     __device__ __forceinline__ bool wide(FwPairs& pr) {
-        const int i = pr.i;
-        FwSide<3> hi, lo;
+        const int i = pr.i, row_bytes = BF16 ? 2 * a.F : a.F;
+        FwSide hi, lo;
         point<2>(hi, i, 0);
         if constexpr (BF16) point<2>(lo, i, a.h_lo);
         FwAcc<3> acc;
         acc.clear();
         do {
-            FwActs<3, true, BLOCK, false> v;
-            fw_fetch(v, hi, pr.k * a.down.chunk, a.F * ES);
+            const int c0 = pr.k * a.down.chunk;
+            FwActs<F, fw_batch<F, true>(), true> v;
+            fw_fetch(v, hi, c0, row_bytes);
             if (!ring.wait(ctx, abort)) return false;
-            fw_mul<BF16>(acc, ring.data(), n, v);
+            fw_mul_stage<F, true>(acc, ring.data(), n, c0, row_bytes, hi, v);
             if constexpr (BF16) {
-                fw_fetch(v, lo, pr.k * a.down.chunk, a.F * ES);
-                fw_mul<BF16>(acc, ring.data(), n, v);
+                fw_fetch(v, lo, c0, row_bytes);
+                fw_mul_stage<F, true>(acc, ring.data(), n, c0, row_bytes, lo, v);
             }
             ring.release();
             pr.step(lst_e, n_list, a.down.n, warp);
@@ -354,11 +353,13 @@ struct FewDown {
         return true;
     }
     __device__ __forceinline__ bool run() {
+        constexpr bool TWO = BF16;   // high and low parts
+        const int row_bytes = BF16 ? 2 * a.F : a.F;
         FwPairs pr{0, 0};
         pr.seek(lst_e, n_list, a.down.n, warp);
         bool fetched = false;
-        FwSide<3> side;
-        FwActs<3, BF16, BLOCK, false> v;
+        FwSide side;
+        FwActs<F, fw_batch<F, TWO>(), TWO> v;
         while (pr.i < n_list) {
             const int i = pr.i;
             if (lst_n[i] > 8) {
@@ -367,20 +368,20 @@ struct FewDown {
             }
             if (!fetched) {
                 point<1>(side, i, 0);
-                fw_fetch(v, side, pr.k * a.down.chunk, a.F * ES);
+                fw_fetch(v, side, pr.k * a.down.chunk, row_bytes);
             }
             FwAcc<3> acc;
             acc.clear();
             do {
                 if (!ring.wait(ctx, abort)) return false;
-                fw_mul<BF16>(acc, ring.data(), n, v);
+                fw_mul_stage<F, TWO>(acc, ring.data(), n, pr.k * a.down.chunk, row_bytes, side, v);
                 ring.release();
                 // the next pair's activations, of this entry or the next
                 pr.step(lst_e, n_list, a.down.n, warp);
                 fetched = pr.i < n_list && lst_n[pr.i] <= 8;
                 if (fetched) {
                     if (pr.i != i) point<1>(side, pr.i, 0);
-                    fw_fetch(v, side, pr.k * a.down.chunk, a.F * ES);
+                    fw_fetch(v, side, pr.k * a.down.chunk, row_bytes);
                 }
             } while (pr.i == i);
             add<1>(acc, i);
@@ -426,6 +427,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     volatile int* slot_piece = reinterpret_cast<volatile int*>(rbar + 1);   // [warp][slot]
     volatile int* abort_flag = slot_piece + FW_WARPS * FW_MAX_STAGES;
     int* n_touched = const_cast<int*>(abort_flag) + 1;
+    int* first_piece = n_touched + 1;
     red.bar = smem_u32(rbar);
     red.turn = 0;
 
@@ -441,6 +443,10 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     for (int i = tid; i < 256; i += FW_THREADS) emask[i] = 0;
     __syncthreads();
     pdl_enter();
+
+    // The CTA's first pieces: an equal share for every CTA of those that there are at least (K experts'),
+    // claimed together; single claims would let the CTAs that start first take more than others.
+    if (tid == 32 * FW_WARPS) *first_piece = a.first > 0 ? atomicAdd(a.counters, a.first) : 0;
 
     // ---- the routing, the same in every CTA
     for (int t = warp; t < a.T; t += FW_WARPS + 1) {
@@ -506,12 +512,6 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     const int n_units = gridDim.x * a.share.units;
     auto unit_row = [&](int u) { return (int)((int64_t)u * a.H / n_units); };
 
-    // A CTA's first pieces are claimed together, an equal share for every CTA and one more while there
-    // are any: single claims would let the CTAs that start first take more than others.
-    const int first = min(n_pieces / (int)gridDim.x, FW_WARPS);
-    if (tid == 0) *n_touched = first > 0 ? atomicAdd(a.counters, first) : 0;
-    __syncthreads();
-
     if (warp == FW_WARPS) {
         // ---- producer: lane w fills ring w stage by stage, its pieces and then its pairs of every unit
         const uint64_t policy = l2_policy_evict_first();
@@ -519,9 +519,12 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
         FwPut put(rings, w);
         volatile int* my_piece = slot_piece + w * FW_MAX_STAGES;
         int y = 0, x = a.up.bytes, n = 0, piece = 0;   // the rows and the byte to fill next
-        int claim = w < first ? *n_touched + w : n_pieces;
         const bool active = lane < FW_WARPS;
-        if (active && w == first) claim = atomicAdd(a.counters, 1);
+        // the rings past the CTA's first share start with a claim of their own as far as there is one
+        // for every CTA's
+        int claim = w < a.first ? *first_piece + w : n_pieces;
+        if (active && w >= a.first && (w - a.first) * (int)gridDim.x < n_pieces - a.first * (int)gridDim.x)
+            claim = atomicAdd(a.counters, 1);
         int unit = -1;                                 // output unit (-1: still in pieces)
         const CUtensorMap* map = nullptr;
         FwPairs pr{0, 0};
@@ -676,7 +679,7 @@ cudaError_t launch_few(const moe_dims* d, const uint16_t* x, const uint16_t* wr,
     r.H = d->H;
     r.E = d->E;
     r.logits = ws.logits;
-    r.xq = fp8 ? ws.xq : nullptr;
+    r.xq = fp8 ? reinterpret_cast<__half*>(ws.xq) : nullptr;
     r.x_scale = fp8 ? sc->x_scale : 1.0f;
     r.counters = ws.counters;
     cudaError_t e = launch_k(few_router_kernel, dim3(d->E + (fp8 ? r.T : 0)), dim3(FEW_RT), 0, stream, r, ctx);
@@ -690,6 +693,7 @@ cudaError_t launch_few(const moe_dims* d, const uint16_t* x, const uint16_t* wr,
     a.topk_w = w;
     a.logits = ws.logits;
     a.act = fp8 ? ws.xq : reinterpret_cast<const uint8_t*>(x);
+    a.first = std::min((d->K + d->Fs / d->F) * (d->F / FEW_PIECE) / num_sms, FW_WARPS);
     a.su = fp8 ? sc->w_up_scale : nullptr;
     a.sd = fp8 ? sc->w_down_scale : nullptr;
     a.x_scale = fp8 ? sc->x_scale : 1.0f;

@@ -59,8 +59,10 @@ inline FwCut fw_cut(int bytes, bool block) {
     return c;
 }
 
-// D (16 tokens x 8 weight rows, fp32) += A (16 x 32 bytes) * B (8 x 32 bytes): bf16 or E4M3 operands
-// (volatile: it must stay where the whole warp is converged).
+// D (16 tokens x 8 weight rows, fp32) += A (16 x 16 values) * B (8 x 16 values), bf16 or fp16 operands
+// (volatile: it must stay where the whole warp is converged).  E4M3 operands are converted to fp16,
+// which holds them exactly: the warp-level E4M3 instruction takes 24 cycles of a scheduler here,
+// against 8 for the fp16 one, and would convert the activations again for every eight weight rows.
 template <bool BF16>
 __device__ __forceinline__ void fw_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
@@ -71,9 +73,17 @@ __device__ __forceinline__ void fw_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
         asm volatile(
-            "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four E4M3 codes as two pairs of fp16 values.
+__device__ __forceinline__ void fw_half4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
 }
 
 // The rings' barriers and slots in shared memory, [warp][slot].
@@ -204,56 +214,73 @@ __device__ __forceinline__ bool fw_produce(FwPut& put, bool active, const Step& 
     return true;
 }
 
-// What goes with the weights of one stage, in registers: 16 bytes per segment of the two activation
-// rows that this lane supplies (rows g and g + 8 of the 16-row operand; TWO: they differ), and the
-// scales of its results.  Fetched while the warp still waits for the weights, or fills its ring.
-template <int NT, bool TWO, bool BLOCK, bool BLOCK_ACT>
-struct FwActs {
-    static constexpr int SEGS = fw_segs(BLOCK), KB = BLOCK ? SEGS / 2 : 1;
-    uint4 x[SEGS][TWO ? 2 : 1];
-    float ws[KB][BLOCK ? NT : 1][2];               // weight rows 8 nt + 2 q, + 1
-    float xs[BLOCK_ACT ? KB : 1][TWO ? 2 : 1];     // activation rows g, g + 8
+// How a stream's operands are held: weights in bf16 (activations too), or in E4M3 with activations as
+// E4M3 codes or as fp16 values; BLOCK: a scale per 128 weights of a row, BLOCK_ACT: of the activations.
+template <bool BF16_, bool CODES_, bool BLOCK_, bool BLOCK_ACT_>
+struct FwFmt {
+    static constexpr bool BF16 = BF16_, CODES = CODES_, BLOCK = BLOCK_, BLOCK_ACT = BLOCK_ACT_;
+    static constexpr int SEGS = fw_segs(BLOCK);
+    static constexpr int AB = BF16 || CODES ? 16 : 32;   // bytes of activations that go with 16 of weights
+    static constexpr int AV = AB / 16;                   // loads for them
 };
 
-// Where they come from: from the start of a K row on, this lane's + 16 q bytes.  A token slot without a
-// token, like a row past the tile, repeats another one and is not used.
-template <int NT>
+// What goes with the weights of N segments, in registers: the two activation rows that this lane
+// supplies (rows g and g + 8 of the 16-row operand; TWO: they differ), the scales of one weight row
+// (row `lane`, handed round by shuffles) and of the two activation rows.  The first batch of a stage is
+// fetched while the warp still waits for its weights.
+template <typename F, int N, bool TWO>
+struct FwActs {
+    static constexpr int KB = F::BLOCK ? N / 2 : 1;
+    static_assert(!F::BLOCK || N % 2 == 0, "whole blocks");
+    uint4 x[N][TWO ? 2 : 1][F::AV];
+    float ws[KB];
+    float xs[F::BLOCK_ACT ? KB : 1][TWO ? 2 : 1];
+};
+
+// Where they come from: from the start of a K row on (activation rows: this lane's first bytes).  A token
+// slot without a token, like a row past the tile, repeats another one and is not used.
 struct FwSide {
     const uint8_t* act[2];
-    const float* ws[NT][2];
+    const float* ws;        // of weight row `lane`
     const float* xs[2];
 };
 
-// Bytes c0 .. of the rows, which hold row_bytes (zeros past them; weights may be padded).
-template <int NT, bool TWO, bool BLOCK, bool BLOCK_ACT>
-__device__ __forceinline__ void fw_fetch(FwActs<NT, TWO, BLOCK, BLOCK_ACT>& v, const FwSide<NT>& side, int c0,
-                                         int row_bytes) {
-    using A = FwActs<NT, TWO, BLOCK, BLOCK_ACT>;
+// The batch from weight byte c0 on; the activation rows go with row_bytes weight bytes (zeros past
+// them; weights may be padded).
+template <typename F, int N, bool TWO>
+__device__ __forceinline__ void fw_fetch(FwActs<F, N, TWO>& v, const FwSide& side, int c0, int row_bytes) {
     const int q16 = (threadIdx.x % 4) * 16;
-    const bool full = c0 + A::SEGS * FW_SEG <= row_bytes;
+    const bool full = c0 + N * FW_SEG <= row_bytes;
+    if (full) {
 #pragma unroll
-    for (int t = 0; t < (TWO ? 2 : 1); ++t) {
-        const uint8_t* p = side.act[t] + c0;
-        if (full) {
+        for (int t = 0; t < (TWO ? 2 : 1); ++t) {
+            const uint8_t* p = side.act[t] + c0 * F::AV;
 #pragma unroll
-            for (int s = 0; s < A::SEGS; ++s) v.x[s][t] = *reinterpret_cast<const uint4*>(p + s * FW_SEG);
-        } else {
+            for (int s = 0; s < N; ++s)
 #pragma unroll
-            for (int s = 0; s < A::SEGS; ++s) {
-                v.x[s][t] = make_uint4(0, 0, 0, 0);
-                if (c0 + s * FW_SEG + q16 < row_bytes) v.x[s][t] = *reinterpret_cast<const uint4*>(p + s * FW_SEG);
-            }
+                for (int j = 0; j < F::AV; ++j)
+                    v.x[s][t][j] = *reinterpret_cast<const uint4*>(p + s * FW_SEG * F::AV + j * 16);
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < (TWO ? 2 : 1); ++t) {
+            const uint8_t* p = side.act[t] + c0 * F::AV;
+#pragma unroll
+            for (int s = 0; s < N; ++s)
+#pragma unroll
+                for (int j = 0; j < F::AV; ++j) {
+                    v.x[s][t][j] = make_uint4(0, 0, 0, 0);
+                    if (c0 + s * FW_SEG + q16 < row_bytes)
+                        v.x[s][t][j] = *reinterpret_cast<const uint4*>(p + s * FW_SEG * F::AV + j * 16);
+                }
         }
     }
-    if constexpr (BLOCK) {
+    if constexpr (F::BLOCK) {
 #pragma unroll
-        for (int b = 0; b < A::KB; ++b) {
+        for (int b = 0; b < FwActs<F, N, TWO>::KB; ++b) {
             const bool in = full || c0 + b * 128 < row_bytes;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) v.ws[b][nt][j] = in ? __ldg(side.ws[nt][j] + c0 / 128 + b) : 0.0f;
-            if constexpr (BLOCK_ACT) {
+            v.ws[b] = in ? __ldg(side.ws + c0 / 128 + b) : 0.0f;
+            if constexpr (F::BLOCK_ACT) {
 #pragma unroll
                 for (int t = 0; t < (TWO ? 2 : 1); ++t) v.xs[b][t] = in ? __ldg(side.xs[t] + c0 / 128 + b) : 0.0f;
             }
@@ -275,43 +302,89 @@ struct FwAcc {
     __device__ __forceinline__ float sum(int nt, int j) const { return d[0][nt][j] + d[1][nt][j]; }
 };
 
-// One stage: `rows` weight rows (at most 8 NT) in the slot, times the activations. (tiles of
-// eight past them are skipped).
-template <bool BF16, int NT, bool TWO, bool BLOCK, bool BLOCK_ACT>
-__device__ __forceinline__ void fw_mul(FwAcc<NT>& acc, const uint8_t* slot, int rows,
-                                       const FwActs<NT, TWO, BLOCK, BLOCK_ACT>& v) {
-    constexpr int SEGS = fw_segs(BLOCK);
-    const int lane = threadIdx.x % 32, g = lane / 4, q16 = (lane % 4) * 16;
+// 16 bytes of weights of one row times the activations that go with them.
+template <typename F, bool TWO>
+__device__ __forceinline__ void fw_step(float (&d0)[4], float (&d1)[4], const uint4 (&x)[TWO ? 2 : 1][F::AV],
+                                        const uint4& w) {
+    if constexpr (F::BF16) {
+        const uint4 a = x[0][0], b = x[TWO ? 1 : 0][0];
+        fw_mma<true>(d0, a.x, b.x, a.y, b.y, w.x, w.y);
+        fw_mma<true>(d1, a.z, b.z, a.w, b.w, w.z, w.w);
+    } else {
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t b0, b1, a[2][2];
+            fw_half4(ww[j], b0, b1);
+#pragma unroll
+            for (int t = 0; t < (TWO ? 2 : 1); ++t) {
+                if constexpr (F::CODES) {
+                    const uint4 c = x[t][0];
+                    fw_half4(j == 0 ? c.x : j == 1 ? c.y : j == 2 ? c.z : c.w, a[t][0], a[t][1]);
+                } else {
+                    const uint4 c = x[t][j / 2];
+                    a[t][0] = j % 2 == 0 ? c.x : c.z;
+                    a[t][1] = j % 2 == 0 ? c.y : c.w;
+                }
+            }
+            fw_mma<false>(j % 2 ? d1 : d0, a[0][0], a[TWO ? 1 : 0][0], a[0][1], a[TWO ? 1 : 0][1], b0, b1);
+        }
+    }
+}
+
+// A batch of N segments from byte b of the slot's rows: `rows` weight rows (at most 8 NT; tiles of eight
+// past them are skipped) times the activations.
+template <typename F, int N, bool TWO, int NT>
+__device__ __forceinline__ void fw_mul(FwAcc<NT>& acc, const uint8_t* slot, int b, int rows, const FwActs<F, N, TWO>& v) {
+    const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         if (nt * 8 >= rows) break;
         // rows past the last repeat it: their results are not used
-        const uint8_t* r = slot + min(nt * 8 + g, rows - 1) * (SEGS * FW_SEG) + q16;
+        const uint8_t* r = slot + min(nt * 8 + g, rows - 1) * (F::SEGS * FW_SEG) + b + q * 16;
         float part[2][4];
 #pragma unroll
-        for (int s = 0; s < SEGS; ++s) {
-            const uint4 a = v.x[s][0], b = v.x[s][TWO ? 1 : 0], w = *reinterpret_cast<const uint4*>(r + s * FW_SEG);
-            if constexpr (BLOCK) {
+        for (int s = 0; s < N; ++s) {
+            const uint4 w = *reinterpret_cast<const uint4*>(r + s * FW_SEG);
+            if constexpr (F::BLOCK) {
                 if (s % 2 == 0) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) part[0][j] = part[1][j] = 0.0f;
                 }
-                fw_mma<BF16>(part[0], a.x, b.x, a.y, b.y, w.x, w.y);
-                fw_mma<BF16>(part[1], a.z, b.z, a.w, b.w, w.z, w.w);
+                fw_step<F, TWO>(part[0], part[1], v.x[s], w);
                 if (s % 2 == 1) {
+                    const float s0 = __shfl_sync(0xffffffffu, v.ws[s / 2], nt * 8 + 2 * q);
+                    const float s1 = __shfl_sync(0xffffffffu, v.ws[s / 2], nt * 8 + 2 * q + 1);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        float sc = v.ws[s / 2][nt][j % 2];
-                        if constexpr (BLOCK_ACT) sc *= v.xs[s / 2][TWO ? j / 2 : 0];
+                        float sc = j % 2 ? s1 : s0;
+                        if constexpr (F::BLOCK_ACT) sc *= v.xs[s / 2][TWO ? j / 2 : 0];
                         float& d = acc.d[s / 2 % 2][nt][j];
                         d = __fmaf_rn(sc, part[0][j] + part[1][j], d);
                     }
                 }
             } else {
-                fw_mma<BF16>(acc.d[0][nt], a.x, b.x, a.y, b.y, w.x, w.y);
-                fw_mma<BF16>(acc.d[1][nt], a.z, b.z, a.w, b.w, w.z, w.w);
+                fw_step<F, TWO>(acc.d[0][nt], acc.d[1][nt], v.x[s], w);
             }
         }
+    }
+}
+
+// The batches of a stage after the first (registers: two activation rows of fp16 take twice the room).
+template <typename F, bool TWO>
+constexpr int fw_batch() {
+    return TWO && F::AV == 2 ? (F::BLOCK ? 2 : 1) : F::SEGS;
+}
+template <typename F, bool TWO, int NT>
+__device__ __forceinline__ void fw_mul_stage(FwAcc<NT>& acc, const uint8_t* slot, int rows, int c0, int row_bytes,
+                                             const FwSide& side, FwActs<F, fw_batch<F, TWO>(), TWO>& v) {
+    constexpr int N = fw_batch<F, TWO>();
+    static_assert(F::SEGS % N == 0, "whole batches");
+    fw_mul(acc, slot, 0, rows, v);
+#pragma unroll 1
+    for (int s = N; s < F::SEGS; s += N) {
+        fw_fetch(v, side, c0 + s * FW_SEG, row_bytes);
+        fw_mul(acc, slot, s * FW_SEG, rows, v);
     }
 }
 

@@ -119,8 +119,8 @@ constexpr int kFewMaxTokens = 16;
 struct FewWs {
     int* counters;        // [2]: unit claims, up reports
     long long* logits;    // [T][E]
-    uint8_t* xq;          // E4M3 codes of x [T][H] (quantised experts)
-    uint8_t* h;           // ReLU^2 rows [T*(K+ns)][F]: E4M3 codes, or bf16 high parts and then low parts
+    uint8_t* xq;          // fp16 values of x's E4M3 codes [T][H] (quantised experts)
+    uint8_t* h;           // ReLU^2 rows [T*(K+ns)][F]: fp16 values of codes, or bf16 high parts, then low parts
 };
 cudaError_t launch_few(const moe_dims* d, const uint16_t* x, const uint16_t* wr, const float* bias, const void* w_up,
                        const void* w_down, const void* w_up_s, const void* w_down_s, const moe_fp8_scales* sc,

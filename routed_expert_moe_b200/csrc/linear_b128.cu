@@ -110,7 +110,8 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     FwTake ring(rings, warp);
     const int g = lane / 4, q = lane % 4;
     const int M = (int)l.M;
-    FwSide<3> side;
+    using F = FwFmt<false, true, true, true>;
+    FwSide side;
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
         const int row = min(t * 8 + g, M - 1);
@@ -123,15 +124,12 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
         FwAcc<3> acc;
         acc.clear();
         if (n > 0 && warp < a.cut.n) {
-#pragma unroll
-            for (int nt = 0; nt < 3; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) side.ws[nt][j] = l.ws + (int64_t)(n0 + min(nt * 8 + 2 * q + j, n - 1)) * l.kb;
-            FwActs<3, TT == 2, true, true> v;
+            side.ws = l.ws + (int64_t)(n0 + min(lane, n - 1)) * l.kb;
+            FwActs<F, fw_batch<F, TT == 2>(), TT == 2> v;
             fw_fetch(v, side, warp * a.cut.chunk, l.Kp);
             for (int k = warp; k < a.cut.n;) {
                 if (!ring.wait(ctx, abort_flag)) return fw_settle();
-                fw_mul<false>(acc, ring.data(), n, v);
+                fw_mul_stage<F, TT == 2>(acc, ring.data(), n, k * a.cut.chunk, l.Kp, side, v);
                 ring.release();
                 k += FW_WARPS;
                 if (k < a.cut.n) fw_fetch(v, side, k * a.cut.chunk, l.Kp);
