@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     if (tid == 32 * FW_WARPS) *first_piece = a.first > 0 ? atomicAdd(a.counters, a.first) : 0;
 
     // ---- the routing, the same in every CTA
-    for (int t = warp; t < a.T; t += FW_WARPS + 1) {
+    for (int t = warp; t < a.T; t += FW_WARPS + FW_PROD) {
         int e;
         float w;
         few_select(a.logits + (int64_t)t * a.E, a.E, a.K, lane, e, w);
@@ -512,14 +512,15 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     const int n_units = gridDim.x * a.share.units;
     auto unit_row = [&](int u) { return (int)((int64_t)u * a.H / n_units); };
 
-    if (warp == FW_WARPS) {
-        // ---- producer: lane w fills ring w stage by stage, its pieces and then its pairs of every unit
+    if (warp >= FW_WARPS) {
+        // ---- producers: a lane fills ring w stage by stage, its pieces and then its pairs of every unit
+        fw_producer_regs();
         const uint64_t policy = l2_policy_evict_first();
-        const int w = lane % FW_WARPS;
+        const bool active = fw_put_lane();
+        const int w = active ? fw_put_ring() : 0;
         FwPut put(rings, w);
         volatile int* my_piece = slot_piece + w * FW_MAX_STAGES;
         int y = 0, x = a.up.bytes, n = 0, piece = 0;   // the rows and the byte to fill next
-        const bool active = lane < FW_WARPS;
         // the rings past the CTA's first share start with a claim of their own as far as there is one
         // for every CTA's
         int claim = w < a.first ? *first_piece + w : n_pieces;
@@ -575,6 +576,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     }
 
     // ---- consumers: pieces
+    fw_consumer_regs();
     FwTake ring(rings, warp);
     while (true) {
         if (!ring.wait(ctx, abort_flag)) return fw_settle();

@@ -4,8 +4,9 @@
 // A weight row is read once from HBM and meets at most 16 activation rows, so
 // the work is a stream: 2 * 16 operations per weight at most, far below what
 // the tensor cores take at HBM's rate.  Each of a CTA's eight consumer warps
-// has a ring in shared memory of its own.  Lane w of the producer warp fills
-// ring w (one TMA box, 16 to 24 rows of a chunk of K, per stage).  A consumer
+// has a ring in shared memory of its own.  A lane of one of four producer
+// warps fills it (one TMA box, 16 to 24 rows of a chunk of K, per stage; with
+// one producer warp the issue of the boxes bounds the stream).  A consumer
 // fetches the activations that go with its next stage into registers, waits
 // for the weights, multiplies with warp-level matrix instructions (tokens as
 // the 16-row operand, weight rows as the 8-column one) and hands the slot
@@ -35,7 +36,8 @@
 namespace moe {
 
 constexpr int FW_WARPS = 8;                   // consumer warps
-constexpr int FW_THREADS = 32 * (FW_WARPS + 1);
+constexpr int FW_PROD = 4;                    // producer warps: one issues a box every 220 cycles at best
+constexpr int FW_THREADS = 32 * (FW_WARPS + FW_PROD);
 constexpr int FW_SEG = 64;                    // bytes of a row that one matrix step takes
 constexpr int FW_ROWS = 24;                   // weight rows per stage at most
 constexpr int FW_MAX_STAGES = 6;              // of one warp's ring
@@ -44,6 +46,13 @@ constexpr int FW_SMEM = 227 * 1024;           // shared memory a block may use
 // Segments per stage.  Five: an odd number puts the rows of a stage, 320 bytes apart, into
 // alternating halves of the banks.  Formats with a scale per 128 bytes take whole blocks.
 constexpr int fw_segs(bool block) { return block ? 6 : 5; }
+
+// Registers: a block of 12 warps starts with 168 per thread.  The consumers' operands need more, the
+// producers' few: 8 warps x 32 x 216 + 4 x 32 x 64 = 63488 of the 64512 that the block holds.
+__device__ __forceinline__ void fw_consumer_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
+__device__ __forceinline__ void fw_producer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
+static_assert(FW_WARPS % 4 == 0 && FW_PROD % 4 == 0, "whole warpgroups");
+static_assert(32 * (FW_WARPS * 216 + FW_PROD * 64) <= 32 * (FW_WARPS + FW_PROD) * 168, "registers of the block");
 
 // How a weight row of `bytes` bytes is cut into chunks (the last one may reach past the row: zeros).
 struct FwCut {
@@ -136,7 +145,7 @@ struct FwTake {
     }
 };
 
-// Producer side of one ring: one lane of the producer warp each.
+// Producer side of one ring: one lane of a producer warp each.
 struct FwPut {
     uint8_t* base;
     uint32_t full, empty;
@@ -182,7 +191,11 @@ struct FwPut {
     }
 };
 
-// The producer warp's loop: step() fills one stage of this lane's ring, false once there is none left.
+// A producer warp's ring, by lane: those of lanes 0 and 1.
+__device__ __forceinline__ int fw_put_ring() { return threadIdx.x / 32 - FW_WARPS + FW_PROD * (threadIdx.x % 32); }
+__device__ __forceinline__ bool fw_put_lane() { return threadIdx.x % 32 < FW_WARPS / FW_PROD; }
+
+// A producer warp's loop: step() fills one stage of this lane's ring, false once there is none left.
 // A lane looks for a free slot without waiting, so that one slow ring does not hold up the others.
 // Ends (false) when no ring made progress for the time limit or a consumer gave up.
 template <typename Step>

@@ -82,9 +82,11 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     const LinearArgs& l = a.l;
     const int n_units = gridDim.x * a.share.units;
     auto unit_row = [&](int u) { return (int)((int64_t)u * l.N / n_units); };
-    if (warp == FW_WARPS) {   // producer: lane w fills ring w, every eighth chunk of each unit
+    if (warp >= FW_WARPS) {   // producers: a lane fills ring w, every eighth chunk of each unit
+        fw_producer_regs();
         const uint64_t policy = l2_policy_evict_first();
-        const int w = lane % FW_WARPS;
+        const bool mine = fw_put_lane();
+        const int w = mine ? fw_put_ring() : 0;
         FwPut put(rings, w);
         int unit = -1, k = 0, n0 = 0, n = 0;
         auto next_unit = [&]() {
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
             } while (n <= 0);
             return true;
         };
-        const bool active = lane < FW_WARPS && next_unit();
+        const bool active = mine && next_unit();
         auto step = [&]() {
             put.fill(&maps.w[a.share.rows - n], k * a.cut.chunk, n0, n * a.cut.chunk, policy);
             k += FW_WARPS;
@@ -107,6 +109,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
         return;
     }
 
+    fw_consumer_regs();
     FwTake ring(rings, warp);
     const int g = lane / 4, q = lane % 4;
     const int M = (int)l.M;
