@@ -24,6 +24,7 @@
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -229,49 +230,44 @@ __device__ __forceinline__ bool few_up(const FewArgs& a, FwTake& ring, int e, in
     constexpr bool BF16 = F::BF16, BLOCK = F::BLOCK;
     const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
     const int row_bytes = BF16 ? 2 * a.H : a.H;
-    FwSide side;
+    FwSide<TT> side;
 #pragma unroll
     for (int t = 0; t < TT; ++t) side.act[t] = a.act + (int64_t)tok[min(t * 8 + g, n_tok - 1)] * a.H * 2 + q * F::AB;
     if constexpr (BLOCK) side.ws = a.su + ((int64_t)e * a.F + f + lane % FEW_PIECE) * (a.up.bytes / 128);
-    FwAcc<2> acc;
+    FwAcc<1, TT> acc;
     acc.clear();
-    FwActs<F, fw_batch<F, TT == 2>(), TT == 2> v;
+    FwActs<F, fw_batch<F, TT>(), TT> v;
     fw_fetch(v, side, 0, row_bytes);
     for (int c0 = 0; c0 < a.up.bytes;) {
         if (!ring.wait(ctx, abort)) return false;
-        fw_mul_stage<F, TT == 2>(acc, ring.data(), FEW_PIECE, c0, row_bytes, side, v);
+        fw_mul_stage(acc, ring.data(), FEW_PIECE, c0, row_bytes, side, v);
         ring.release();
         c0 += a.up.chunk;
         if (c0 < a.up.bytes) fw_fetch(v, side, c0, row_bytes);
     }
     const float sc = BF16 ? 1.0f : BLOCK ? a.x_scale : __fmul_rn(a.su[e], a.x_scale);
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-        if (t * 8 + g >= n_tok) continue;
+    for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            const int64_t o = (int64_t)rowi[t * 8 + g] * a.F + f + nt * 8 + 2 * q;
-            float h[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float z = acc.sum(nt, 2 * t + j);
-                if constexpr (!BF16) z = __fmul_rn(z, sc);
-                h[j] = z <= 0.0f ? 0.0f : __fmul_rn(z, z);   // a NaN stays one
-            }
+        for (int j = 0; j < 4; ++j) {
+            const int s = t * 8 + 2 * q + j % 2;
+            if (s >= n_tok) continue;
+            const int64_t o = (int64_t)rowi[s] * a.F + f + g + 8 * (j / 2);
+            float z = acc.sum(0, t, j);
+            if constexpr (!BF16) z = __fmul_rn(z, sc);
+            const float h = z <= 0.0f ? 0.0f : __fmul_rn(z, z);   // a NaN stays one
             if constexpr (BF16) {
                 // h as the sum of two bf16, 16 bits of it: one alone would add a second rounding of the
                 // output's size
-                const __nv_bfloat162 hi = __floats2bfloat162_rn(h[0], h[1]);
-                const float t0 = __low2float(hi), t1 = __high2float(hi), inf = __uint_as_float(0x7f800000u);
-                *reinterpret_cast<__nv_bfloat162*>(a.h + 2 * o) = hi;
-                *reinterpret_cast<__nv_bfloat162*>(a.h + a.h_lo + 2 * o) =
-                    __floats2bfloat162_rn(t0 < inf ? __fsub_rn(h[0], t0) : 0.0f, t1 < inf ? __fsub_rn(h[1], t1) : 0.0f);
+                const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+                const float top = __bfloat162float(hi);
+                reinterpret_cast<__nv_bfloat16*>(a.h)[o] = hi;
+                reinterpret_cast<__nv_bfloat16*>(a.h + a.h_lo)[o] =
+                    __float2bfloat16_rn(top < __uint_as_float(0x7f800000u) ? __fsub_rn(h, top) : 0.0f);
             } else {
-                *reinterpret_cast<uint32_t*>(a.h + 2 * o) =
-                    few_code_values(__fdiv_rn(h[0], a.h_scale), __fdiv_rn(h[1], a.h_scale));
+                reinterpret_cast<uint16_t*>(a.h)[o] = (uint16_t)few_code_values(__fdiv_rn(h, a.h_scale), 0.0f);
             }
         }
-    }
     return true;
 }
 
@@ -292,74 +288,101 @@ struct FewDown {
     const DevCtx& ctx;
     volatile int* abort;
 
-    // Entry i: activation rows (lo: bf16 low parts), weight scales
-    template <int TT>
-    __device__ __forceinline__ void point(FwSide& side, int i, int64_t lo) const {
+    // Entry i: the activations of its first 8 TT token slots (bf16, TT 1: high and low parts), weight scales
+    template <int NT>
+    __device__ __forceinline__ void point(FwSide<NT>& side, int i, bool parts) const {
         const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
         const int last = lst_n[i] - 1;
-        side.act[0] = a.h + (int64_t)rowi[i * 16 + min(g, last)] * a.F * 2 + q * F::AB + lo;
-        if constexpr (TT == 2) side.act[1] = a.h + (int64_t)rowi[i * 16 + min(8 + g, last)] * a.F * 2 + q * F::AB + lo;
-        else if constexpr (BF16) side.act[1] = side.act[0] + a.h_lo;   // the low parts are rows 8 .. 15
+        side.act[0] = a.h + (int64_t)rowi[i * 16 + min(g, last)] * a.F * 2 + q * F::AB;
+        if constexpr (NT == 2)
+            side.act[1] = parts ? side.act[0] + a.h_lo : a.h + (int64_t)rowi[i * 16 + min(8 + g, last)] * a.F * 2 + q * F::AB;
         if constexpr (BLOCK) side.ws = a.sd + ((int64_t)lst_e[i] * a.H + d0 + min(lane, n - 1)) * (a.down.bytes / 128);
     }
+    // The running sums of one entry and a stage of them
+    template <int NT>
+    struct Acc {
+        typename std::conditional<BF16, FwAccT<3>, FwAcc<2, NT>>::type s;
+    };
+    template <int NT>
+    __device__ __forceinline__ void mul(Acc<NT>& acc, int c0, int row_bytes, const FwSide<NT>& side,
+                                        FwActs<F, fw_batch<F, NT>(), NT>& v) const {
+        if constexpr (BF16) fw_mul_t(acc.s, ring.data(), n, v);
+        else fw_mul_stage(acc.s, ring.data(), n, c0, row_bytes, side, v);
+    }
     // Weighted sums of entry i, for the tokens routed to it only
-    template <int TT>
-    __device__ __forceinline__ void add(const FwAcc<3>& acc, int i) const {
+    template <int NT>
+    __device__ __forceinline__ void add(const Acc<NT>& acc, int i, bool parts) const {
         const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
-        const float sc = FMT == MOE_FP8_E4M3 ? a.sd[lst_e[i]] : 1.0f;
+        if constexpr (BF16) {
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const int s = t * 8 + g;
-            if (s >= lst_n[i]) continue;
-            const float w = wt[i * 16 + s] * sc;
+            for (int t = 0; t < 2; ++t) {
+                const int s = t * 8 + g;
+                if (s >= lst_n[i] || (t == 1 && parts)) continue;
+                const float w = wt[i * 16 + s];
 #pragma unroll
-            for (int nt = 0; nt < 3; ++nt) {
-                float2* p = reinterpret_cast<float2*>(tot + tok[i * 16 + s] * FW_ROWS + nt * 8 + 2 * q);
-                float2 v = *p;
-                float y0 = acc.sum(nt, 2 * t), y1 = acc.sum(nt, 2 * t + 1);
-                if constexpr (BF16 && TT == 1) {
-                    y0 += acc.sum(nt, 2);
-                    y1 += acc.sum(nt, 3);
+                for (int nt = 0; nt < 3; ++nt) {
+                    float2* p = reinterpret_cast<float2*>(tot + tok[i * 16 + s] * FW_ROWS + nt * 8 + 2 * q);
+                    float y0 = acc.s.sum(nt, 2 * t), y1 = acc.s.sum(nt, 2 * t + 1);
+                    if (parts) {
+                        y0 += acc.s.sum(nt, 2);
+                        y1 += acc.s.sum(nt, 3);
+                    }
+                    const float2 v = *p;
+                    *p = make_float2(__fmaf_rn(w, y0, v.x), __fmaf_rn(w, y1, v.y));
                 }
-                v.x = __fmaf_rn(w, y0, v.x);
-                v.y = __fmaf_rn(w, y1, v.y);
-                *p = v;
             }
+        } else {
+            const float sc = FMT == MOE_FP8_E4M3 ? a.sd[lst_e[i]] : 1.0f;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int s = t * 8 + 2 * q + c;
+                    if (s >= lst_n[i]) continue;
+                    const float w = wt[i * 16 + s] * sc;
+                    float* p = tot + tok[i * 16 + s] * FW_ROWS + g;
+#pragma unroll
+                    for (int r = 0; r < 3; ++r)   // rows g + 8 r
+                        p[8 * r] = __fmaf_rn(w, acc.s.sum(r / 2, t, c + 2 * (r % 2)), p[8 * r]);
+                }
         }
         __syncwarp();
     }
     // An entry with more than eight tokens
     __device__ __forceinline__ bool wide(FwPairs& pr) {
         const int i = pr.i, row_bytes = BF16 ? 2 * a.F : a.F;
-        FwSide hi, lo;
-        point<2>(hi, i, 0);
-        if constexpr (BF16) point<2>(lo, i, a.h_lo);
-        FwAcc<3> acc;
-        acc.clear();
+        FwSide<2> hi, lo;
+        point<2>(hi, i, false);
+        if constexpr (BF16) {
+            lo.act[0] = hi.act[0] + a.h_lo;
+            lo.act[1] = hi.act[1] + a.h_lo;
+        }
+        Acc<2> acc;
+        acc.s.clear();
         do {
             const int c0 = pr.k * a.down.chunk;
-            FwActs<F, fw_batch<F, true>(), true> v;
+            FwActs<F, fw_batch<F, 2>(), 2> v;
             fw_fetch(v, hi, c0, row_bytes);
             if (!ring.wait(ctx, abort)) return false;
-            fw_mul_stage<F, true>(acc, ring.data(), n, c0, row_bytes, hi, v);
+            mul(acc, c0, row_bytes, hi, v);
             if constexpr (BF16) {
                 fw_fetch(v, lo, c0, row_bytes);
-                fw_mul_stage<F, true>(acc, ring.data(), n, c0, row_bytes, lo, v);
+                mul(acc, c0, row_bytes, lo, v);
             }
             ring.release();
             pr.step(lst_e, n_list, a.down.n, warp);
         } while (pr.i == i);
-        add<2>(acc, i);
+        add(acc, i, false);
         return true;
     }
     __device__ __forceinline__ bool run() {
-        constexpr bool TWO = BF16;   // high and low parts
+        constexpr int NT = BF16 ? 2 : 1;   // high and low parts
         const int row_bytes = BF16 ? 2 * a.F : a.F;
         FwPairs pr{0, 0};
         pr.seek(lst_e, n_list, a.down.n, warp);
         bool fetched = false;
-        FwSide side;
-        FwActs<F, fw_batch<F, TWO>(), TWO> v;
+        FwSide<NT> side;
+        FwActs<F, fw_batch<F, NT>(), NT> v;
         while (pr.i < n_list) {
             const int i = pr.i;
             if (lst_n[i] > 8) {
@@ -367,24 +390,24 @@ struct FewDown {
                 continue;
             }
             if (!fetched) {
-                point<1>(side, i, 0);
+                point<NT>(side, i, true);
                 fw_fetch(v, side, pr.k * a.down.chunk, row_bytes);
             }
-            FwAcc<3> acc;
-            acc.clear();
+            Acc<NT> acc;
+            acc.s.clear();
             do {
                 if (!ring.wait(ctx, abort)) return false;
-                fw_mul_stage<F, TWO>(acc, ring.data(), n, pr.k * a.down.chunk, row_bytes, side, v);
+                mul(acc, pr.k * a.down.chunk, row_bytes, side, v);
                 ring.release();
                 // the next pair's activations, of this entry or the next
                 pr.step(lst_e, n_list, a.down.n, warp);
                 fetched = pr.i < n_list && lst_n[pr.i] <= 8;
                 if (fetched) {
-                    if (pr.i != i) point<1>(side, pr.i, 0);
+                    if (pr.i != i) point<NT>(side, pr.i, true);
                     fw_fetch(v, side, pr.k * a.down.chunk, row_bytes);
                 }
             } while (pr.i == i);
-            add<1>(acc, i);
+            add(acc, i, true);
         }
         return true;
     }

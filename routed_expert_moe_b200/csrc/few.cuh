@@ -8,9 +8,8 @@
 // warps fills it (one TMA box, 16 to 24 rows of a chunk of K, per stage; with
 // one producer warp the issue of the boxes bounds the stream).  A consumer
 // fetches the activations that go with its next stage into registers, waits
-// for the weights, multiplies with warp-level matrix instructions (tokens as
-// the 16-row operand, weight rows as the 8-column one) and hands the slot
-// back.  No consumer waits for another within a stream.  tcgen05 would need
+// for the weights, multiplies with warp-level matrix instructions (weights as
+// the 16-row operand, tokens as the 8-column one) and hands the slot back.  No consumer waits for another within a stream.  tcgen05 would need
 // 128 weight rows per instruction; boxes of 16 to 24 rows let every SM stream
 // the same number of bytes.
 //
@@ -20,9 +19,9 @@
 // on it.
 //
 // Lane (g, q) = (lane / 4, lane % 4) of a warp reads 16 bytes at
-// 64 * segment + 16 * q of weight rows g, g + 8, g + 16 and of tokens g and g + 8:
-// the matrix instruction's K index is assigned to those bytes in the same
-// order on both sides, so no value moves between lanes.
+// 64 * segment + 16 * q of weight rows 16 m + g and 16 m + g + 8 and of token
+// g's activations: the matrix instruction's K index is assigned to those bytes
+// in the same order on both sides, so no value moves between lanes.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -43,9 +42,9 @@ constexpr int FW_ROWS = 24;                   // weight rows per stage at most
 constexpr int FW_MAX_STAGES = 6;              // of one warp's ring
 constexpr int FW_SMEM = 227 * 1024;           // shared memory a block may use
 
-// Segments per stage.  Five: an odd number puts the rows of a stage, 320 bytes apart, into
+// Segments per stage.  Seven: an odd number puts the rows of a stage, 448 bytes apart, into
 // alternating halves of the banks.  Formats with a scale per 128 bytes take whole blocks.
-constexpr int fw_segs(bool block) { return block ? 6 : 5; }
+constexpr int fw_segs(bool block) { return block ? 6 : 7; }
 
 // Registers: a block of 12 warps starts with 168 per thread.  The consumers' operands need more, the
 // producers' few: 8 warps x 32 x 216 + 4 x 32 x 64 = 63488 of the 64512 that the block holds.
@@ -68,10 +67,10 @@ inline FwCut fw_cut(int bytes, bool block) {
     return c;
 }
 
-// D (16 tokens x 8 weight rows, fp32) += A (16 x 16 values) * B (8 x 16 values), bf16 or fp16 operands
+// D (16 weight rows x 8 tokens, fp32) += A (16 x 16 values) * B (8 x 16 values), bf16 or fp16 operands
 // (volatile: it must stay where the whole warp is converged).  E4M3 operands are converted to fp16,
 // which holds them exactly: the warp-level E4M3 instruction takes 24 cycles of a scheduler here,
-// against 8 for the fp16 one, and would convert the activations again for every eight weight rows.
+// against 8 for the fp16 one.
 template <bool BF16>
 __device__ __forceinline__ void fw_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
@@ -237,36 +236,36 @@ struct FwFmt {
     static constexpr int AV = AB / 16;                   // loads for them
 };
 
-// What goes with the weights of N segments, in registers: the two activation rows that this lane
-// supplies (rows g and g + 8 of the 16-row operand; TWO: they differ), the scales of one weight row
-// (row `lane`, handed round by shuffles) and of the two activation rows.  The first batch of a stage is
-// fetched while the warp still waits for its weights.
-template <typename F, int N, bool TWO>
+// What goes with the weights of N segments, in registers: the activations of this lane's NT columns
+// (g + 8 nt), the scales of weight row `lane` and of column `lane`, handed round by shuffles.  A stage's
+// first batch is fetched while the warp still waits for its weights.
+template <typename F, int N, int NT>
 struct FwActs {
     static constexpr int KB = F::BLOCK ? N / 2 : 1;
     static_assert(!F::BLOCK || N % 2 == 0, "whole blocks");
-    uint4 x[N][TWO ? 2 : 1][F::AV];
+    uint4 x[N][NT][F::AV];
     float ws[KB];
-    float xs[F::BLOCK_ACT ? KB : 1][TWO ? 2 : 1];
+    float xs[F::BLOCK_ACT ? KB : 1];
 };
 
-// Where they come from: from the start of a K row on (activation rows: this lane's first bytes).  A token
-// slot without a token, like a row past the tile, repeats another one and is not used.
+// Where they come from: from the start of a K row on (activations: this lane's first bytes).  A column
+// without a token, like a row past the tile, repeats another one and is not used.
+template <int NT>
 struct FwSide {
-    const uint8_t* act[2];
+    const uint8_t* act[NT];
     const float* ws;        // of weight row `lane`
-    const float* xs[2];
+    const float* xs;        // of column `lane`
 };
 
 // The batch from weight byte c0 on; the activation rows go with row_bytes weight bytes (zeros past
 // them; weights may be padded).
-template <typename F, int N, bool TWO>
-__device__ __forceinline__ void fw_fetch(FwActs<F, N, TWO>& v, const FwSide& side, int c0, int row_bytes) {
+template <typename F, int N, int NT>
+__device__ __forceinline__ void fw_fetch(FwActs<F, N, NT>& v, const FwSide<NT>& side, int c0, int row_bytes) {
     const int q16 = (threadIdx.x % 4) * 16;
     const bool full = c0 + N * FW_SEG <= row_bytes;
     if (full) {
 #pragma unroll
-        for (int t = 0; t < (TWO ? 2 : 1); ++t) {
+        for (int t = 0; t < NT; ++t) {
             const uint8_t* p = side.act[t] + c0 * F::AV;
 #pragma unroll
             for (int s = 0; s < N; ++s)
@@ -276,7 +275,7 @@ __device__ __forceinline__ void fw_fetch(FwActs<F, N, TWO>& v, const FwSide& sid
         }
     } else {
 #pragma unroll
-        for (int t = 0; t < (TWO ? 2 : 1); ++t) {
+        for (int t = 0; t < NT; ++t) {
             const uint8_t* p = side.act[t] + c0 * F::AV;
 #pragma unroll
             for (int s = 0; s < N; ++s)
@@ -290,22 +289,146 @@ __device__ __forceinline__ void fw_fetch(FwActs<F, N, TWO>& v, const FwSide& sid
     }
     if constexpr (F::BLOCK) {
 #pragma unroll
-        for (int b = 0; b < FwActs<F, N, TWO>::KB; ++b) {
+        for (int b = 0; b < FwActs<F, N, NT>::KB; ++b) {
             const bool in = full || c0 + b * 128 < row_bytes;
             v.ws[b] = in ? __ldg(side.ws + c0 / 128 + b) : 0.0f;
-            if constexpr (F::BLOCK_ACT) {
-#pragma unroll
-                for (int t = 0; t < (TWO ? 2 : 1); ++t) v.xs[b][t] = in ? __ldg(side.xs[t] + c0 / 128 + b) : 0.0f;
-            }
+            if constexpr (F::BLOCK_ACT) v.xs[b] = in ? __ldg(side.xs + c0 / 128 + b) : 0.0f;
         }
     }
 }
 
-// The running sums of 16 activation rows x 8 NT weight rows, in two chains that do not wait for one
-// another.  j: activation row g (+ 8 * (j / 2)), weight row 8 nt + 2 q + j % 2.
-template <int NT>
+// The running sums of 16 MT weight rows x 8 NT columns.  j: weight row 16 mt + g + 8 * (j / 2), column
+// 8 nt + 2 q + j % 2.  A matrix instruction takes 21 cycles and a scheduler starts one every 8, so
+// small tiles keep two chains of sums.
+template <int MT, int NT>
 struct FwAcc {
-    float d[2][NT][4];
+    static constexpr int kChains = MT * NT >= 4 ? 1 : 2;
+    float d[kChains][MT][NT][4];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int c = 0; c < kChains; ++c)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) d[c][mt][nt][j] = 0.0f;
+    }
+    __device__ __forceinline__ float sum(int mt, int nt, int j) const {
+        return kChains == 1 ? d[0][mt][nt][j] : d[0][mt][nt][j] + d[kChains - 1][mt][nt][j];
+    }
+};
+
+// 4 bytes (step j of 4) of weights of rows g (w0) and g + 8 (w1) of every tile times the activations that
+// go with them: a quarter of 16 bytes of E4M3, or (even j) half of 16 bytes of bf16.
+template <typename F, int MT, int NT>
+__device__ __forceinline__ void fw_step(float (&d)[MT][NT][4], const uint4 (&x)[NT][F::AV], const uint4 (&w0)[MT],
+                                        const uint4 (&w1)[MT], int j) {
+    if constexpr (F::BF16) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint4 u = w0[mt], v = w1[mt], b = x[nt][0];
+                if (j == 0) fw_mma<true>(d[mt][nt], u.x, v.x, u.y, v.y, b.x, b.y);
+                if (j == 2) fw_mma<true>(d[mt][nt], u.z, v.z, u.w, v.w, b.z, b.w);
+            }
+    } else {
+        uint32_t b[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const uint4 c = x[nt][F::CODES ? 0 : j / 2];
+            if constexpr (F::CODES) {
+                fw_half4(j == 0 ? c.x : j == 1 ? c.y : j == 2 ? c.z : c.w, b[nt][0], b[nt][1]);
+            } else {
+                b[nt][0] = j % 2 == 0 ? c.x : c.z;
+                b[nt][1] = j % 2 == 0 ? c.y : c.w;
+            }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const uint4 u = w0[mt], v = w1[mt];
+            uint32_t a0, a1, a2, a3;
+            fw_half4(j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w, a0, a2);
+            fw_half4(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w, a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) fw_mma<false>(d[mt][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+        }
+    }
+}
+
+// A batch of N segments from byte b of the slot's rows: `rows` weight rows (at most 16 MT) times the
+// activations.
+template <typename F, int N, int MT, int NT>
+__device__ __forceinline__ void fw_mul(FwAcc<MT, NT>& acc, const uint8_t* slot, int b, int rows, const FwActs<F, N, NT>& v) {
+    constexpr int C = FwAcc<MT, NT>::kChains;
+    const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
+    const uint8_t *r0[MT], *r1[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {   // rows past the last repeat it: their results are not used
+        r0[mt] = slot + min(mt * 16 + g, rows - 1) * (F::SEGS * FW_SEG) + b + q * 16;
+        r1[mt] = slot + min(mt * 16 + g + 8, rows - 1) * (F::SEGS * FW_SEG) + b + q * 16;
+    }
+    float part[C][MT][NT][4];
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+        uint4 w0[MT], w1[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            w0[mt] = *reinterpret_cast<const uint4*>(r0[mt] + s * FW_SEG);
+            w1[mt] = *reinterpret_cast<const uint4*>(r1[mt] + s * FW_SEG);
+        }
+        if constexpr (F::BLOCK) {
+            if (s % 2 == 0) {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) part[c][mt][nt][j] = 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) fw_step<F, MT, NT>(part[j % C], v.x[s], w0, w1, j);
+            if (s % 2 == 1) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const float s0 = __shfl_sync(0xffffffffu, v.ws[s / 2], mt * 16 + g);
+                    const float s1 = __shfl_sync(0xffffffffu, v.ws[s / 2], mt * 16 + g + 8);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float x0 = 1.0f, x1 = 1.0f;
+                        if constexpr (F::BLOCK_ACT) {
+                            x0 = __shfl_sync(0xffffffffu, v.xs[s / 2], nt * 8 + 2 * q);
+                            x1 = __shfl_sync(0xffffffffu, v.xs[s / 2], nt * 8 + 2 * q + 1);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float sc = j / 2 ? s1 : s0;
+                            if constexpr (F::BLOCK_ACT) sc *= j % 2 ? x1 : x0;
+                            float p = part[0][mt][nt][j];
+                            if constexpr (C == 2) p += part[C - 1][mt][nt][j];
+                            acc.d[0][mt][nt][j] = __fmaf_rn(sc, p, acc.d[0][mt][nt][j]);
+                        }
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; j += F::BF16 ? 2 : 1)
+                fw_step<F, MT, NT>(acc.d[(F::BF16 ? j / 2 : j) % C], v.x[s], w0, w1, j);
+        }
+    }
+}
+
+// The other way round, for bf16 activations that come in two parts: 16 rows of activations (two sets of
+// eight, FwActs' columns) times 8 NT weight rows.  The low parts ride in the operand's second half, and
+// the 17 to 24 weight rows of a unit are three tiles of eight instead of two of 16: six instructions a
+// segment against eight (layer of 16 tokens: 241 against 283 us).
+template <int NT>
+struct FwAccT {
+    float d[2][NT][4];   // j: activation row g (+ 8 * (j / 2)), weight row 8 nt + 2 q + j % 2
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -314,84 +437,34 @@ struct FwAcc {
     }
     __device__ __forceinline__ float sum(int nt, int j) const { return d[0][nt][j] + d[1][nt][j]; }
 };
-
-// 16 bytes of weights of one row times the activations that go with them.
-template <typename F, bool TWO>
-__device__ __forceinline__ void fw_step(float (&d0)[4], float (&d1)[4], const uint4 (&x)[TWO ? 2 : 1][F::AV],
-                                        const uint4& w) {
-    if constexpr (F::BF16) {
-        const uint4 a = x[0][0], b = x[TWO ? 1 : 0][0];
-        fw_mma<true>(d0, a.x, b.x, a.y, b.y, w.x, w.y);
-        fw_mma<true>(d1, a.z, b.z, a.w, b.w, w.z, w.w);
-    } else {
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t b0, b1, a[2][2];
-            fw_half4(ww[j], b0, b1);
-#pragma unroll
-            for (int t = 0; t < (TWO ? 2 : 1); ++t) {
-                if constexpr (F::CODES) {
-                    const uint4 c = x[t][0];
-                    fw_half4(j == 0 ? c.x : j == 1 ? c.y : j == 2 ? c.z : c.w, a[t][0], a[t][1]);
-                } else {
-                    const uint4 c = x[t][j / 2];
-                    a[t][0] = j % 2 == 0 ? c.x : c.z;
-                    a[t][1] = j % 2 == 0 ? c.y : c.w;
-                }
-            }
-            fw_mma<false>(j % 2 ? d1 : d0, a[0][0], a[TWO ? 1 : 0][0], a[0][1], a[TWO ? 1 : 0][1], b0, b1);
-        }
-    }
-}
-
-// A batch of N segments from byte b of the slot's rows: `rows` weight rows (at most 8 NT; tiles of eight
-// past them are skipped) times the activations.
-template <typename F, int N, bool TWO, int NT>
-__device__ __forceinline__ void fw_mul(FwAcc<NT>& acc, const uint8_t* slot, int b, int rows, const FwActs<F, N, TWO>& v) {
+template <typename F, int N, int NT>
+__device__ __forceinline__ void fw_mul_t(FwAccT<NT>& acc, const uint8_t* slot, int rows, const FwActs<F, N, 2>& v) {
+    static_assert(F::BF16, "bf16 in two parts");
     const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         if (nt * 8 >= rows) break;
         // rows past the last repeat it: their results are not used
-        const uint8_t* r = slot + min(nt * 8 + g, rows - 1) * (F::SEGS * FW_SEG) + b + q * 16;
-        float part[2][4];
+        const uint8_t* r = slot + min(nt * 8 + g, rows - 1) * (F::SEGS * FW_SEG) + q * 16;
 #pragma unroll
         for (int s = 0; s < N; ++s) {
-            const uint4 w = *reinterpret_cast<const uint4*>(r + s * FW_SEG);
-            if constexpr (F::BLOCK) {
-                if (s % 2 == 0) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) part[0][j] = part[1][j] = 0.0f;
-                }
-                fw_step<F, TWO>(part[0], part[1], v.x[s], w);
-                if (s % 2 == 1) {
-                    const float s0 = __shfl_sync(0xffffffffu, v.ws[s / 2], nt * 8 + 2 * q);
-                    const float s1 = __shfl_sync(0xffffffffu, v.ws[s / 2], nt * 8 + 2 * q + 1);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float sc = j % 2 ? s1 : s0;
-                        if constexpr (F::BLOCK_ACT) sc *= v.xs[s / 2][TWO ? j / 2 : 0];
-                        float& d = acc.d[s / 2 % 2][nt][j];
-                        d = __fmaf_rn(sc, part[0][j] + part[1][j], d);
-                    }
-                }
-            } else {
-                fw_step<F, TWO>(acc.d[0][nt], acc.d[1][nt], v.x[s], w);
-            }
+            const uint4 a = v.x[s][0][0], b = v.x[s][1][0], w = *reinterpret_cast<const uint4*>(r + s * FW_SEG);
+            fw_mma<true>(acc.d[0][nt], a.x, b.x, a.y, b.y, w.x, w.y);
+            fw_mma<true>(acc.d[1][nt], a.z, b.z, a.w, b.w, w.z, w.w);
         }
     }
 }
 
-// The batches of a stage after the first (registers: two activation rows of fp16 take twice the room).
-template <typename F, bool TWO>
+// Segments fetched together (registers: two columns of fp16 take twice the room of one).
+template <typename F, int NT>
 constexpr int fw_batch() {
-    return TWO && F::AV == 2 ? (F::BLOCK ? 2 : 1) : F::SEGS;
+    return NT == 2 && F::AV == 2 ? (F::BLOCK ? 2 : 1) : F::SEGS;
 }
-template <typename F, bool TWO, int NT>
-__device__ __forceinline__ void fw_mul_stage(FwAcc<NT>& acc, const uint8_t* slot, int rows, int c0, int row_bytes,
-                                             const FwSide& side, FwActs<F, fw_batch<F, TWO>(), TWO>& v) {
-    constexpr int N = fw_batch<F, TWO>();
+// A whole stage, whose first batch has been fetched.
+template <typename F, int MT, int NT>
+__device__ __forceinline__ void fw_mul_stage(FwAcc<MT, NT>& acc, const uint8_t* slot, int rows, int c0, int row_bytes,
+                                             const FwSide<NT>& side, FwActs<F, fw_batch<F, NT>(), NT>& v) {
+    constexpr int N = fw_batch<F, NT>();
     static_assert(F::SEGS % N == 0, "whole batches");
     fw_mul(acc, slot, 0, rows, v);
 #pragma unroll 1

@@ -114,25 +114,25 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     const int g = lane / 4, q = lane % 4;
     const int M = (int)l.M;
     using F = FwFmt<false, true, true, true>;
-    FwSide side;
+    FwSide<TT> side;
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
         const int row = min(t * 8 + g, M - 1);
         side.act[t] = l.xq + (int64_t)row * l.Kp + q * 16;
-        side.xs[t] = l.xs + (int64_t)row * l.kb;
     }
+    side.xs = l.xs + (int64_t)min(lane, M - 1) * l.kb;
     for (int un = 0; un < a.share.units; ++un) {
         const int u = blockIdx.x * a.share.units + un;
         const int n0 = unit_row(u), n = unit_row(u + 1) - n0;
-        FwAcc<3> acc;
+        FwAcc<2, TT> acc;
         acc.clear();
         if (n > 0 && warp < a.cut.n) {
             side.ws = l.ws + (int64_t)(n0 + min(lane, n - 1)) * l.kb;
-            FwActs<F, fw_batch<F, TT == 2>(), TT == 2> v;
+            FwActs<F, fw_batch<F, TT>(), TT> v;
             fw_fetch(v, side, warp * a.cut.chunk, l.Kp);
             for (int k = warp; k < a.cut.n;) {
                 if (!ring.wait(ctx, abort_flag)) return fw_settle();
-                fw_mul_stage<F, TT == 2>(acc, ring.data(), n, k * a.cut.chunk, l.Kp, side, v);
+                fw_mul_stage(acc, ring.data(), n, k * a.cut.chunk, l.Kp, side, v);
                 ring.release();
                 k += FW_WARPS;
                 if (k < a.cut.n) fw_fetch(v, side, k * a.cut.chunk, l.Kp);
@@ -142,9 +142,10 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int nt = 0; nt < 3; ++nt)
-                *reinterpret_cast<float2*>(mine + (t * 8 + g) * FW_ROWS + nt * 8 + 2 * q) =
-                    make_float2(acc.sum(nt, 2 * t), acc.sum(nt, 2 * t + 1));
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int r = 0; r < 3; ++r)   // rows g + 8 r
+                    mine[(t * 8 + 2 * q + c) * FW_ROWS + g + 8 * r] = acc.sum(r / 2, t, c + 2 * (r % 2));
         if (!red.exchange(ctx, abort_flag)) return fw_settle();
         for (int j = tid; j < n * M; j += 32 * FW_WARPS) {
             const int t = j / n, row = j - t * n;
