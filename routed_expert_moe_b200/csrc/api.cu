@@ -226,10 +226,11 @@ ForwardWs carve_forward(Carve& c, void* base, const moe_dims* d) {
 FewWs carve_few(Carve& c, void* base, const moe_dims* d) {
     FewWs f;
     const bool fp8 = d->expert_dtype != MOE_BF16;
-    f.counters = c.take<int>(base, 2);
+    f.counters = c.take<int>(base, (size_t)few_counters(d));
     f.logits = c.take<long long>(base, (size_t)d->T * d->E);
-    f.xq = fp8 ? c.take<uint8_t>(base, (size_t)d->T * d->H * 2) : nullptr;
-    f.h = c.take<uint8_t>(base, (size_t)ffn_rows(d) * d->F * (fp8 ? 2 : 4));
+    f.xq = fp8 ? c.take<uint8_t>(base, (size_t)d->T * d->H) : nullptr;
+    f.h = c.take<uint8_t>(base, (size_t)ffn_rows(d) * d->F * (fp8 ? 1 : 4));
+    f.y = c.take<float>(base, (size_t)ffn_rows(d) * d->H);
     return f;
 }
 

@@ -10,27 +10,31 @@
 // 1. few_router_kernel: one block per expert computes its exact logits for all tokens (few enough
 //    tokens that the exact sum costs less than an approximate one with a bound and a second pass);
 //    further blocks quantise x.  It zeroes the second kernel's counters.
-// 2. few_layer_kernel, persistent, one CTA of eight warps per SM: every CTA ranks the logits itself
-//    (the same integers give the same choice everywhere), lists the touched experts, and then its
-//    consumer warps stream weights (few.cuh): up pieces (16 rows of one expert, claimed for single warps),
-//    then the CTA's share of the output rows through all touched experts, so that the weighted sum
-//    over experts, the residual and the one rounding happen in the CTA that holds them.  The
-//    ring of a warp without further up pieces takes down weights while the last pieces report.
+// 2. few_layer_kernel, persistent, one CTA per SM: every CTA ranks the logits itself (the same
+//    integers give the same choice everywhere) and lists the touched experts; then the CTAs claim units
+//    of 128 weight rows (up units of all entries, then down units) from a counter and multiply them on
+//    the tensor cores: weights as the 128-row operand through a TMA ring, the tokens as 16 columns.
+//      up:   columns are all T tokens (x itself, no gather); the epilogue keeps those that the entry has
+//      down: columns are the entry's rows of h (the rows that follow, of other entries, are not used)
+//    A down unit waits until its entry's up units have reported.  The warp that finishes the last
+//    entry of 32 output rows sums them over the experts, with the residual, in one rounding.
 //
-// Up pieces are claimed from a counter, so those that a warp waits for belong to warps that run and
-// that wait for nothing; no CTA needs another to be resident, and every wait is bounded.
+// Units are claimed in list order, so those that a unit waits for belong to CTAs that run; no CTA
+// needs another to be resident, and every wait is bounded.
 //
-// Bound: HBM bytes of the touched experts' weights.
+// Bound: HBM bytes of the touched experts' weights.  128-row units leave SMs without work at one or two
+// tokens (87 up units at one token of the full sizes), which costs little: a load-only loop of 60 MB
+// takes 16.4 us on 87 SMs and on 148.
 #include <algorithm>
 #include <climits>
 #include <cstdint>
-#include <type_traits>
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "few.cuh"
+#include "common.cuh"
+#include "internal.h"
 
 namespace moe {
 
@@ -44,18 +48,11 @@ struct FewRouterArgs {
     const float* bias;
     int T, H, E;
     long long* logits;   // [T][E], units of 2^-40
-    __half* xq;          // values of x's E4M3 codes [T][H], or null
+    uint8_t* xq;         // E4M3 codes of x [T][H], or null
     float x_scale;
-    int* counters;       // [2]: piece claims, piece reports
+    int* counters;       // of the second kernel: zeroed here
+    int n_counters;
 };
-
-// The E4M3 codes (nearest-even, saturating) of two quotients, as a pair of fp16 values.
-__device__ __forceinline__ uint32_t few_code_values(float a, float b) {
-    const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    uint32_t lo, hi;
-    fw_half4(c, lo, hi);
-    return lo;
-}
 
 __global__ void __launch_bounds__(FEW_RT) few_router_kernel(FewRouterArgs a, DevCtx ctx) {
     pdl_enter();
@@ -63,23 +60,25 @@ __global__ void __launch_bounds__(FEW_RT) few_router_kernel(FewRouterArgs a, Dev
     __shared__ float s_x[kFewMaxTokens][8], s_w[8];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int nv = a.H / 8;
-    if ((int)blockIdx.x >= a.E) {   // one token's E4M3 codes, as values
+    if ((int)blockIdx.x >= a.E) {   // one token's E4M3 codes
         const int t = blockIdx.x - a.E;
         const uint4* xr = reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.H);
         for (int v = tid; v < nv; v += FEW_RT) {
             const uint4 p = xr[v];
             const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-            uint32_t c[4];
+            uint32_t c[2] = {0, 0};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                c[j] = few_code_values(__fdiv_rn(__uint_as_float(w[j] << 16), a.x_scale),
-                                       __fdiv_rn(__uint_as_float(w[j] & 0xFFFF0000u), a.x_scale));
-            reinterpret_cast<uint4*>(a.xq + (int64_t)t * a.H)[v] = make_uint4(c[0], c[1], c[2], c[3]);
+            for (int j = 0; j < 8; ++j) {
+                const float f = __uint_as_float((j & 1) ? (w[j / 2] & 0xFFFF0000u) : (w[j / 2] << 16));
+                c[j / 4] |= (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(f, a.x_scale), __NV_SATFINITE, __NV_E4M3)
+                            << (8 * (j % 4));
+            }
+            reinterpret_cast<uint2*>(a.xq + (int64_t)t * a.H)[v] = make_uint2(c[0], c[1]);
         }
         return;
     }
     const int e = blockIdx.x;
-    if (e == 0 && tid < 2) a.counters[tid] = 0;
+    for (int i = e * FEW_RT + tid; i < a.n_counters; i += a.E * FEW_RT) a.counters[i] = 0;
     // a warp takes one token over 1 / parts of H
     const int parts = a.T == 1 ? 8 : a.T == 2 ? 4 : a.T <= 4 ? 2 : 1;
     const int part = warp % parts;
@@ -134,43 +133,63 @@ __global__ void __launch_bounds__(FEW_RT) few_router_kernel(FewRouterArgs a, Dev
 
 // ----------------------------------------------------------------------------- layer
 
+constexpr int FL_THREADS = 512;     // weights, two of products, four of the epilogue, columns; all route
+constexpr int FL_MMA = 2;           // warps that issue products: of the even and of the odd stages
+constexpr int FL_BM = 128;          // weight rows per unit
+constexpr int FL_KB = 128;          // bytes of K per stage (E4M3: one scale block)
+constexpr int FL_A = FL_BM * FL_KB;
+constexpr int FL_N = 16;            // token columns
+constexpr int FL_B = FL_N * FL_KB;
+constexpr int FL_UQ = 4;            // unit queue slots
+constexpr int FL_MAX_STAGES = 12;
+constexpr int FL_SMEM = 227 * 1024;
+// Bytes of each shared matrix that are fetched into L2 while the routing is found.
+constexpr int64_t kFewWarmBytes = (int64_t)24 << 20;
+static_assert(kFewMaxTokens == FL_N, "a token per column");
+
+template <int FMT>
+struct FlShape {
+    static constexpr bool BF16 = FMT == MOE_BF16, BLOCK = FMT == MOE_FP8_B128;
+    static constexpr int kStage = FL_A + (BF16 ? 2 : 1) * FL_B;   // bf16: low parts of h beside the high ones
+    // TMEM results: of a scale block, of a unit.  Each is kept as several sums: instructions that add to
+    // the same columns wait for one another, and the two issuing threads are not ordered.  bf16: 32
+    // columns each, the second 16 for the low parts of h.
+    static constexpr int kCols = BF16 ? 2 * FL_N : FL_N;
+    static constexpr int kSums = BLOCK ? 2 : 2 * FL_MMA;
+    static constexpr int kSlots = BLOCK ? 8 : 2;
+    static constexpr int kTmem = kSlots * kSums * kCols;
+};
+
+// Weights in boxes of 128 and of 64 rows (the last rows of an expert), tokens and h in boxes of 16.
+struct FewMaps {
+    CUtensorMap up128, up64, down128, down64, ups128, ups64, downs128, downs64, x, h;
+};
+
 struct FewArgs {
-    const uint16_t* x;
     const uint16_t* residual;   // or null
     uint16_t* out;
     int32_t* topk_idx;          // or null
     float* topk_w;              // or null
     const long long* logits;
-    const uint8_t* act;         // up operand rows [T][H]: x, or the fp16 values of its E4M3 codes
-    const float* su;            // E4M3: [E]; B128: [E][F][kbu]
-    const float* sd;            // E4M3: [E]; B128: [E][H][kbd]
+    const float* su;            // E4M3: [E]; B128: [E][F][k_up]
+    const float* sd;            // E4M3: [E]; B128: [E][H][k_down]
     float x_scale, h_scale;
-    uint8_t* h;                 // [rows][F]: bf16 high parts and then low parts, or fp16 values of E4M3 codes
-    int64_t h_lo;               // bf16: bytes from a high part to its low part
-    int* counters;
+    uint8_t* h;                 // [rows][F] in list order: E4M3 codes; bf16 high parts, then all low parts
+    float* y;                   // [T*K + ns*T][H]: expert outputs of assignment t*K + k, then shared chunks
+    int* counters;              // claim | reports per entry [n_list_max] | entries done per 32 output rows
+    const uint8_t* warm[2];     // shared expert: weights to fetch into L2 while the routing is found
+    int64_t warm_bytes;         // of each
     int T, H, E, K, F, ns;
-    FwCut up, down;
-    FwShare share;              // of the output rows
-    int slot_bytes, n_stages;
-    int n_list_max;
-    int first;                  // pieces that a CTA claims at the start
-    int hold;                   // test hook: up piece 0 never reports
+    int k_up, k_down;           // stages per unit
+    int m_up, m_down;           // units per entry
+    int n_stages, n_list_max;
+    int hold;                   // test hook: the first up unit never reports
 };
 
-// Weight matrices: rows of W_up in boxes of 16; rows of W_down in boxes of share.rows and one less;
-// the same of the shared expert.
-struct FewMaps {
-    CUtensorMap up, down[2], up_s, down_s[2];
-};
-
-constexpr int FEW_PIECE = 16;   // rows of an up piece (F is a multiple of 16)
-
-// shared memory after the rings: reduction buffers | wt [n][16] f32 | rowi [n][16] u16 | tok [n][16] u8 |
-// lst_e [n] i32 | lst_n [n] i32 | emask [256] i32 | slot [256] i32 | sel_w [16][16] f32 | sel_e [16][16] i32 |
-// barriers | piece of each slot | flags
+// shared memory after the ring: barriers | queue, flags | lst_e, lst_mask, lst_off [n] i32 | rowi [n][16] u16 |
+// emask, eslot [256] i32 | sel_w [16][16] f32 | sel_e [16][16] i32
 __host__ __device__ inline size_t few_table_bytes(int n_list) {
-    return (size_t)n_list * (64 + 32 + 16 + 8) + 16 + 4 * 1024 + FwRings::kBarBytes + 8 +
-           FW_WARPS * FW_MAX_STAGES * 4 + 16;
+    return (2 * FL_MAX_STAGES + 2 * 8 + FL_MMA + 2 * FL_UQ) * 8 + (FL_UQ + 4) * 4 + (size_t)n_list * (3 * 4 + 32) + 4 * 1024 + 16;
 }
 
 // The K best experts of one token (one warp): by logit, ties to the lower index; lane k returns the
@@ -219,476 +238,513 @@ __device__ __forceinline__ void few_select(const long long* row, int E, int K, i
     my_w = ex / z;
 }
 
-template <int FMT>
-using FewFmt = FwFmt<FMT == MOE_BF16, false, FMT == MOE_FP8_B128, false>;
-
-// One up piece: 16 rows of a list entry with at most 8 TT tokens.
-template <int FMT, int TT>
-__device__ __forceinline__ bool few_up(const FewArgs& a, FwTake& ring, int e, int f, int n_tok, const uint16_t* rowi,
-                                       const uint8_t* tok, const DevCtx& ctx, volatile int* abort) {
-    using F = FewFmt<FMT>;
-    constexpr bool BF16 = F::BF16, BLOCK = F::BLOCK;
-    const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
-    const int row_bytes = BF16 ? 2 * a.H : a.H;
-    FwSide<TT> side;
-#pragma unroll
-    for (int t = 0; t < TT; ++t) side.act[t] = a.act + (int64_t)tok[min(t * 8 + g, n_tok - 1)] * a.H * 2 + q * F::AB;
-    if constexpr (BLOCK) side.ws = a.su + ((int64_t)e * a.F + f + lane % FEW_PIECE) * (a.up.bytes / 128);
-    FwAcc<1, TT> acc;
-    acc.clear();
-    FwActs<F, fw_batch<F, TT>(), TT> v;
-    fw_fetch(v, side, 0, row_bytes);
-    for (int c0 = 0; c0 < a.up.bytes;) {
-        if (!ring.wait(ctx, abort)) return false;
-        fw_mul_stage(acc, ring.data(), FEW_PIECE, c0, row_bytes, side, v);
-        ring.release();
-        c0 += a.up.chunk;
-        if (c0 < a.up.bytes) fw_fetch(v, side, c0, row_bytes);
-    }
-    const float sc = BF16 ? 1.0f : BLOCK ? a.x_scale : __fmul_rn(a.su[e], a.x_scale);
-#pragma unroll
-    for (int t = 0; t < TT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int s = t * 8 + 2 * q + j % 2;
-            if (s >= n_tok) continue;
-            const int64_t o = (int64_t)rowi[s] * a.F + f + g + 8 * (j / 2);
-            float z = acc.sum(0, t, j);
-            if constexpr (!BF16) z = __fmul_rn(z, sc);
-            const float h = z <= 0.0f ? 0.0f : __fmul_rn(z, z);   // a NaN stays one
-            if constexpr (BF16) {
-                // h as the sum of two bf16, 16 bits of it: one alone would add a second rounding of the
-                // output's size
-                const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-                const float top = __bfloat162float(hi);
-                reinterpret_cast<__nv_bfloat16*>(a.h)[o] = hi;
-                reinterpret_cast<__nv_bfloat16*>(a.h + a.h_lo)[o] =
-                    __float2bfloat16_rn(top < __uint_as_float(0x7f800000u) ? __fsub_rn(h, top) : 0.0f);
-            } else {
-                reinterpret_cast<uint16_t*>(a.h)[o] = (uint16_t)few_code_values(__fdiv_rn(h, a.h_scale), 0.0f);
-            }
-        }
-    return true;
+__device__ __forceinline__ void fl_ld16(uint32_t taddr, uint32_t (&v)[FL_N]) {   // no wait
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
 }
 
-// One warp's part of n output rows from d0 on, through its pairs of all list entries: the weighted sums
-// tot [token][row] (shared memory, this warp's).
+// This lane's row of a result: its sums added up, for a down unit of bf16 with those of the low parts.
+// one: a unit of a single stage, whose other sums were not written.
 template <int FMT>
-struct FewDown {
-    using F = FewFmt<FMT>;
-    static constexpr bool BF16 = F::BF16, BLOCK = F::BLOCK;
-    const FewArgs& a;
-    FwTake& ring;
-    const int *lst_e, *lst_n;
-    const uint16_t* rowi;
-    const uint8_t* tok;
-    const float* wt;
-    int n_list, warp, d0, n;
-    float* tot;
-    const DevCtx& ctx;
-    volatile int* abort;
+__device__ __forceinline__ void fl_read(uint32_t addr, bool down, bool one, float (&z)[FL_N]) {
+    using S = FlShape<FMT>;
+    uint32_t p[S::kSums][FL_N];
+#pragma unroll
+    for (int s = 0; s < S::kSums; ++s) fl_ld16(addr + s * S::kCols, p[s]);
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int c = 0; c < FL_N; ++c) {
+        z[c] = __uint_as_float(p[0][c]);
+#pragma unroll
+        for (int s = 1; s < S::kSums; ++s)
+            if (s < 2 || !one) z[c] += __uint_as_float(p[s][c]);
+    }
+    if (S::BF16 && down) {
+#pragma unroll
+        for (int s = 0; s < S::kSums; ++s) fl_ld16(addr + s * S::kCols + FL_N, p[s]);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+        for (int c = 0; c < FL_N; ++c)
+#pragma unroll
+            for (int s = 0; s < S::kSums; ++s)
+                if (s < 2 || !one) z[c] += __uint_as_float(p[s][c]);
+    }
+}
 
-    // Entry i: the activations of its first 8 TT token slots (bf16, TT 1: high and low parts), weight scales
-    template <int NT>
-    __device__ __forceinline__ void point(FwSide<NT>& side, int i, bool parts) const {
-        const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
-        const int last = lst_n[i] - 1;
-        side.act[0] = a.h + (int64_t)rowi[i * 16 + min(g, last)] * a.F * 2 + q * F::AB;
-        if constexpr (NT == 2)
-            side.act[1] = parts ? side.act[0] + a.h_lo : a.h + (int64_t)rowi[i * 16 + min(8 + g, last)] * a.F * 2 + q * F::AB;
-        if constexpr (BLOCK) side.ws = a.sd + ((int64_t)lst_e[i] * a.H + d0 + min(lane, n - 1)) * (a.down.bytes / 128);
-    }
-    // The running sums of one entry and a stage of them
-    template <int NT>
-    struct Acc {
-        typename std::conditional<BF16, FwAccT<3>, FwAcc<2, NT>>::type s;
-    };
-    template <int NT>
-    __device__ __forceinline__ void mul(Acc<NT>& acc, int c0, int row_bytes, const FwSide<NT>& side,
-                                        FwActs<F, fw_batch<F, NT>(), NT>& v) const {
-        if constexpr (BF16) fw_mul_t(acc.s, ring.data(), n, v);
-        else fw_mul_stage(acc.s, ring.data(), n, c0, row_bytes, side, v);
-    }
-    // Weighted sums of entry i, for the tokens routed to it only
-    template <int NT>
-    __device__ __forceinline__ void add(const Acc<NT>& acc, int i, bool parts) const {
-        const int lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
-        if constexpr (BF16) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int s = t * 8 + g;
-                if (s >= lst_n[i] || (t == 1 && parts)) continue;
-                const float w = wt[i * 16 + s];
-#pragma unroll
-                for (int nt = 0; nt < 3; ++nt) {
-                    float2* p = reinterpret_cast<float2*>(tot + tok[i * 16 + s] * FW_ROWS + nt * 8 + 2 * q);
-                    float y0 = acc.s.sum(nt, 2 * t), y1 = acc.s.sum(nt, 2 * t + 1);
-                    if (parts) {
-                        y0 += acc.s.sum(nt, 2);
-                        y1 += acc.s.sum(nt, 3);
-                    }
-                    const float2 v = *p;
-                    *p = make_float2(__fmaf_rn(w, y0, v.x), __fmaf_rn(w, y1, v.y));
-                }
-            }
-        } else {
-            const float sc = FMT == MOE_FP8_E4M3 ? a.sd[lst_e[i]] : 1.0f;
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int s = t * 8 + 2 * q + c;
-                    if (s >= lst_n[i]) continue;
-                    const float w = wt[i * 16 + s] * sc;
-                    float* p = tot + tok[i * 16 + s] * FW_ROWS + g;
-#pragma unroll
-                    for (int r = 0; r < 3; ++r)   // rows g + 8 r
-                        p[8 * r] = __fmaf_rn(w, acc.s.sum(r / 2, t, c + 2 * (r % 2)), p[8 * r]);
-                }
-        }
-        __syncwarp();
-    }
-    // An entry with more than eight tokens
-    __device__ __forceinline__ bool wide(FwPairs& pr) {
-        const int i = pr.i, row_bytes = BF16 ? 2 * a.F : a.F;
-        FwSide<2> hi, lo;
-        point<2>(hi, i, false);
-        if constexpr (BF16) {
-            lo.act[0] = hi.act[0] + a.h_lo;
-            lo.act[1] = hi.act[1] + a.h_lo;
-        }
-        Acc<2> acc;
-        acc.s.clear();
-        do {
-            const int c0 = pr.k * a.down.chunk;
-            FwActs<F, fw_batch<F, 2>(), 2> v;
-            fw_fetch(v, hi, c0, row_bytes);
-            if (!ring.wait(ctx, abort)) return false;
-            mul(acc, c0, row_bytes, hi, v);
-            if constexpr (BF16) {
-                fw_fetch(v, lo, c0, row_bytes);
-                mul(acc, c0, row_bytes, lo, v);
-            }
-            ring.release();
-            pr.step(lst_e, n_list, a.down.n, warp);
-        } while (pr.i == i);
-        add(acc, i, false);
-        return true;
-    }
-    __device__ __forceinline__ bool run() {
-        constexpr int NT = BF16 ? 2 : 1;   // high and low parts
-        const int row_bytes = BF16 ? 2 * a.F : a.F;
-        FwPairs pr{0, 0};
-        pr.seek(lst_e, n_list, a.down.n, warp);
-        bool fetched = false;
-        FwSide<NT> side;
-        FwActs<F, fw_batch<F, NT>(), NT> v;
-        while (pr.i < n_list) {
-            const int i = pr.i;
-            if (lst_n[i] > 8) {
-                if (!wide(pr)) return false;
-                continue;
-            }
-            if (!fetched) {
-                point<NT>(side, i, true);
-                fw_fetch(v, side, pr.k * a.down.chunk, row_bytes);
-            }
-            Acc<NT> acc;
-            acc.s.clear();
-            do {
-                if (!ring.wait(ctx, abort)) return false;
-                mul(acc, pr.k * a.down.chunk, row_bytes, side, v);
-                ring.release();
-                // the next pair's activations, of this entry or the next
-                pr.step(lst_e, n_list, a.down.n, warp);
-                fetched = pr.i < n_list && lst_n[pr.i] <= 8;
-                if (fetched) {
-                    if (pr.i != i) point<NT>(side, pr.i, true);
-                    fw_fetch(v, side, pr.k * a.down.chunk, row_bytes);
-                }
-            } while (pr.i == i);
-            add(acc, i, true);
-        }
-        return true;
-    }
-};
+// The stage of K that a unit begins with.  Every CTA reads the same columns (x, or one entry's rows of
+// h): in step, all of them would ask one L2 slice for the same lines.  It goes by expert and block alone,
+// so that a row's sum does not hang on the batch.
+__device__ __forceinline__ int fl_first(int e, int blk, int k_stages) { return (e * 5 + blk * 11) % k_stages; }
 
 template <int FMT>
-__global__ void __launch_bounds__(FW_THREADS, 1)
+__global__ void __launch_bounds__(FL_THREADS, 1)
     few_layer_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs a, DevCtx ctx) {
-    constexpr int ES = FMT == MOE_BF16 ? 2 : 1;
-    extern __shared__ __align__(1024) uint8_t few_smem[];
+    using S = FlShape<FMT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const int NS = a.n_stages;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)NS * S::kStage);
+    uint64_t* empty = full + FL_MAX_STAGES;
+    uint64_t* rfull = empty + FL_MAX_STAGES;   // TMEM results
+    uint64_t* rempty = rfull + 8;
+    uint64_t* drain = rempty + 8;
+    uint64_t* uq_full = drain + FL_MMA;
+    uint64_t* uq_empty = uq_full + FL_UQ;
+    volatile int* uq = reinterpret_cast<volatile int*>(uq_empty + FL_UQ);
+    volatile int* abort_flag = uq + FL_UQ;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(const_cast<int*>(abort_flag + 1));
+    int* n_touched = reinterpret_cast<int*>(tmem_holder + 1);
+    float(*sel_w)[16] = reinterpret_cast<float(*)[16]>(n_touched + 2);
+    int(*sel_e)[16] = reinterpret_cast<int(*)[16]>(sel_w + 16);
+    int* emask = &sel_e[16][0];
+    int* eslot = emask + 256;
+    int* lst_e = eslot + 256;
+    int* lst_mask = lst_e + a.n_list_max;
+    int* lst_off = lst_mask + a.n_list_max;
+    uint16_t* rowi = reinterpret_cast<uint16_t*>(lst_off + a.n_list_max);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    uint8_t* p = few_smem + (size_t)FW_WARPS * a.n_stages * a.slot_bytes;
-    FwRed red;
-    red.buf = reinterpret_cast<float*>(p);
-    p += FwRed::bytes(a.share.units);
-    float* wt = reinterpret_cast<float*>(p);
-    p += (size_t)a.n_list_max * 64;
-    uint16_t* rowi = reinterpret_cast<uint16_t*>(p);
-    p += (size_t)a.n_list_max * 32;
-    uint8_t* tok = p;
-    p += (size_t)a.n_list_max * 16;
-    int* lst_e = reinterpret_cast<int*>(p);
-    int* lst_n = lst_e + a.n_list_max;
-    p += ((size_t)a.n_list_max * 8 + 15) / 16 * 16;
-    int* emask = reinterpret_cast<int*>(p);
-    p += 1024;
-    int* eslot = reinterpret_cast<int*>(p);
-    p += 1024;
-    float(*sel_w)[16] = reinterpret_cast<float(*)[16]>(p);
-    p += 1024;
-    int(*sel_e)[16] = reinterpret_cast<int(*)[16]>(p);
-    p += 1024;
-    FwRings rings;
-    rings.base = few_smem;
-    rings.full = reinterpret_cast<uint64_t*>(p);
-    rings.empty = rings.full + FW_WARPS * FW_MAX_STAGES;
-    rings.slot_bytes = a.slot_bytes;
-    rings.n = a.n_stages;
-    uint64_t* rbar = rings.full + FwRings::kBarBytes / 8;
-    volatile int* slot_piece = reinterpret_cast<volatile int*>(rbar + 1);   // [warp][slot]
-    volatile int* abort_flag = slot_piece + FW_WARPS * FW_MAX_STAGES;
-    int* n_touched = const_cast<int*>(abort_flag) + 1;
-    int* first_piece = n_touched + 1;
-    red.bar = smem_u32(rbar);
-    red.turn = 0;
 
     if (tid == 0) {
-        rings.init();
-        mbar_init(smem_u32(rbar), FW_WARPS);
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int p = 0; p < S::kSlots; ++p) {
+            mbar_init(smem_u32(&rfull[p]), S::BLOCK ? 1 : FL_MMA);
+            mbar_init(smem_u32(&rempty[p]), 4);
+        }
+        for (int m = 0; m < FL_MMA; ++m) mbar_init(smem_u32(drain + m), 1);
+        for (int q = 0; q < FL_UQ; ++q) {
+            mbar_init(smem_u32(&uq_full[q]), 1);
+            mbar_init(smem_u32(&uq_empty[q]), 1 + FL_MMA + 4);   // columns, products, epilogue warps
+        }
         *abort_flag = 0;
         fence_mbar_init();
-        tma_prefetch_desc(&maps.up);
-        tma_prefetch_desc(&maps.down[0]);
-        tma_prefetch_desc(&maps.down[1]);
+        tma_prefetch_desc(&maps.up128);
+        tma_prefetch_desc(&maps.down128);
+        tma_prefetch_desc(&maps.x);
+        tma_prefetch_desc(&maps.h);
     }
-    for (int i = tid; i < 256; i += FW_THREADS) emask[i] = 0;
+    if (warp == 1) tmem_alloc(smem_u32(tmem_holder), S::kTmem);
+    if (warp == 2 && a.warm_bytes > 0) {
+        // weights are inputs that no kernel before this one writes, and a prefetch changes no data
+        constexpr int64_t piece = 16 * 1024;
+        const int64_t n = (a.warm_bytes + piece - 1) / piece;
+        for (int64_t i = (int64_t)blockIdx.x * 32 + lane; i < 2 * n; i += (int64_t)gridDim.x * 32) {
+            const int64_t off = (i >= n ? i - n : i) * piece;
+            bulk_prefetch_l2(a.warm[i >= n] + off, (uint32_t)min(piece, a.warm_bytes - off));
+        }
+    }
+    for (int i = tid; i < 256; i += FL_THREADS) emask[i] = 0;
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
     pdl_enter();
 
-    // The CTA's first pieces: an equal share for every CTA of those that there are at least (K experts'),
-    // claimed together; single claims would let the CTAs that start first take more than others.
-    if (tid == 32 * FW_WARPS) *first_piece = a.first > 0 ? atomicAdd(a.counters, a.first) : 0;
-
-    // ---- the routing, the same in every CTA
-    for (int t = warp; t < a.T; t += FW_WARPS + FW_PROD) {
+    // ---- the routing, the same in every CTA: one warp per token
+    if (warp < a.T) {
         int e;
         float w;
-        few_select(a.logits + (int64_t)t * a.E, a.E, a.K, lane, e, w);
+        few_select(a.logits + (int64_t)warp * a.E, a.E, a.K, lane, e, w);
         if (lane < a.K) {
-            sel_e[t][lane] = e;
-            sel_w[t][lane] = w;
-            atomicOr(&emask[e], 1 << t);
+            sel_e[warp][lane] = e;
+            sel_w[warp][lane] = w;
+            atomicOr(&emask[e], 1 << warp);
             if (blockIdx.x == 0) {
-                if (a.topk_idx) a.topk_idx[t * a.K + lane] = e;
-                if (a.topk_w) a.topk_w[t * a.K + lane] = w;
+                if (a.topk_idx) a.topk_idx[warp * a.K + lane] = e;
+                if (a.topk_w) a.topk_w[warp * a.K + lane] = w;
             }
         }
     }
     __syncthreads();
     if (warp == 0) {   // the touched experts, ascending, then the shared expert's chunks
-        int n = 0;
+        int n = 0, off = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             const int e = e0 + lane;
             const int mask = e < a.E ? emask[e] : 0;
             const uint32_t m = __ballot_sync(0xffffffffu, mask != 0);
+            int pre = __popc(mask);   // rows of h before this expert's: an inclusive scan
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, pre, d);
+                if (lane >= d) pre += v;
+            }
             if (mask) {
                 const int i = n + __popc(m & ((1u << lane) - 1u));
                 eslot[e] = i;
                 lst_e[i] = e;
-                lst_n[i] = __popc(mask);
+                lst_mask[i] = mask;
+                lst_off[i] = off + pre - __popc(mask);
             }
+            off += __shfl_sync(0xffffffffu, pre, 31);
             n += __popc(m);
         }
         if (lane < a.ns) {
             lst_e[n + lane] = a.E + lane;
-            lst_n[n + lane] = a.T;
+            lst_mask[n + lane] = (1 << a.T) - 1;
+            lst_off[n + lane] = a.T * (a.K + lane);
         }
         if (lane == 0) *n_touched = n;
     }
     __syncthreads();
     const int n_routed = *n_touched, n_list = n_routed + a.ns;
-    // each list entry's tokens, ascending, with the row of h and the weight that go with them
-    for (int i = tid; i < a.T * (a.K + a.ns); i += FW_THREADS) {
+    const int rows = a.T * (a.K + a.ns);
+    // each entry's rows of y, in the order of its tokens
+    for (int i = tid; i < rows; i += FL_THREADS) {
         const int t = i % a.T, k = i / a.T;
-        int s, row;
-        float w;
-        if (k < a.K) {
-            const int e = sel_e[t][k];
-            s = eslot[e] * 16 + __popc(emask[e] & ((1 << t) - 1));
-            row = t * a.K + k;
-            w = sel_w[t][k];
-        } else {
-            s = (n_routed + k - a.K) * 16 + t;
-            row = a.T * a.K + (k - a.K) * a.T + t;
-            w = 1.0f;
-        }
-        rowi[s] = (uint16_t)row;
-        tok[s] = (uint8_t)t;
-        wt[s] = w;
+        const int e = k < a.K ? sel_e[t][k] : 0;
+        const int s = k < a.K ? eslot[e] * 16 + __popc(emask[e] & ((1 << t) - 1)) : (n_routed + k - a.K) * 16 + t;
+        rowi[s] = (uint16_t)(k < a.K ? t * a.K + k : a.T * k + t);
     }
     __syncthreads();
 
-    // ---- work
-    const int per = a.F / FEW_PIECE, n_pieces = n_list * per;   // pieces of one expert, of all
-    const int n_units = gridDim.x * a.share.units;
-    auto unit_row = [&](int u) { return (int)((int64_t)u * a.H / n_units); };
+    const int n_up = n_list * a.m_up, n_units = n_up + n_list * a.m_down;
+    int* done = a.counters + 1;                  // per entry: epilogue warps of up units
+    int* summed = done + a.n_list_max;           // per 32 output rows: entries whose product is stored
 
-    if (warp >= FW_WARPS) {
-        // ---- producers: a lane fills ring w stage by stage, its pieces and then its pairs of every unit
-        fw_producer_regs();
-        const uint64_t policy = l2_policy_evict_first();
-        const bool active = fw_put_lane();
-        const int w = active ? fw_put_ring() : 0;
-        FwPut put(rings, w);
-        volatile int* my_piece = slot_piece + w * FW_MAX_STAGES;
-        int y = 0, x = a.up.bytes, n = 0, piece = 0;   // the rows and the byte to fill next
-        // the rings past the CTA's first share start with a claim of their own as far as there is one
-        // for every CTA's
-        int claim = w < a.first ? *first_piece + w : n_pieces;
-        if (active && w >= a.first && (w - a.first) * (int)gridDim.x < n_pieces - a.first * (int)gridDim.x)
-            claim = atomicAdd(a.counters, 1);
-        int unit = -1;                                 // output unit (-1: still in pieces)
-        const CUtensorMap* map = nullptr;
-        FwPairs pr{0, 0};
-        auto next_unit = [&]() {   // to the next output unit with something for this ring
-            do {
-                if (++unit == a.share.units) return false;
-                const int u = blockIdx.x * a.share.units + unit;
-                y = unit_row(u);
-                n = unit_row(u + 1) - y;
-                pr.i = 0;
-                pr.seek(lst_e, n_list, a.down.n, w);
-            } while (n <= 0 || pr.i >= n_list);
-            return true;
-        };
-        auto step = [&]() {
-            if (unit < 0) {
-                if (x >= a.up.bytes) {
-                    piece = claim;
-                    if (piece >= n_pieces) {   // the consumer's sign that there is no further piece
-                        my_piece[put.slot] = n_pieces;
-                        put.mark();
-                        return next_unit();
-                    }
-                    const int i = piece / per, e = lst_e[i], f = (piece - i * per) * FEW_PIECE;
-                    x = 0;
-                    map = e < a.E ? &maps.up : &maps.up_s;
-                    y = (e < a.E ? e : e - a.E) * a.F + f;
+    // A consumer's next unit from the queue (single thread)
+    auto next_unit = [&](int& qs, uint32_t& qph, int& u) {
+        if (!mbar_wait(smem_u32(&uq_full[qs]), qph, ctx, abort_flag)) return false;
+        u = uq[qs];
+        mbar_arrive(smem_u32(&uq_empty[qs]));
+        if (++qs == FL_UQ) {
+            qs = 0;
+            qph ^= 1u;
+        }
+        return u >= 0;
+    };
+    auto settle = [&]() {   // copies in flight land before the block may end
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 200000ull) __nanosleep(1000);
+    };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- units and their weights
+        if (lane == 0) {
+            const uint64_t policy = l2_policy_evict_first();
+            int stage = 0, qs = 0;
+            uint32_t phase = 0, qph = 0;
+            bool ok = true;
+            int claim = atomicAdd(a.counters, 1);
+            while (ok) {
+                const int u = claim < n_units ? claim : -1;
+                if (!mbar_wait(smem_u32(&uq_empty[qs]), qph ^ 1u, ctx, abort_flag)) {
+                    ok = false;
+                    break;
                 }
-                my_piece[put.slot] = piece;
-                put.fill(map, x, y, FEW_PIECE * a.up.chunk, policy);
-                x += a.up.chunk;
-                // the next piece is claimed one stage before it is needed
-                if (x >= a.up.bytes) claim = atomicAdd(a.counters, 1);
-                return true;
+                uq[qs] = u;
+                mbar_arrive(smem_u32(&uq_full[qs]));
+                if (++qs == FL_UQ) {
+                    qs = 0;
+                    qph ^= 1u;
+                }
+                if (u < 0) break;
+                const bool up = u < n_up;
+                const int v = up ? u : u - n_up, mb = up ? a.m_up : a.m_down;
+                const int i = v / mb, blk = v - i * mb, r0 = blk * FL_BM, e = lst_e[i], n_out = up ? a.F : a.H;
+                const int k_stages = up ? a.k_up : a.k_down;
+                const bool whole = n_out - r0 > 64, shd = e >= a.E;
+                const CUtensorMap* map = up ? (shd ? (whole ? &maps.ups128 : &maps.ups64) : (whole ? &maps.up128 : &maps.up64))
+                                            : (shd ? (whole ? &maps.downs128 : &maps.downs64)
+                                                   : (whole ? &maps.down128 : &maps.down64));
+                // shared chunk j: rows j F .. of its up matrix, columns j F .. of its down matrix (past the
+                // chunk's end the next one's weights meet columns of zeros)
+                const int y = shd ? (up ? (e - a.E) * a.F + r0 : r0) : e * n_out + r0;
+                const int x0 = shd && !up ? (e - a.E) * a.F * 2 : 0;
+                // bytes of the stage: these rows and the columns that the other producer loads
+                const uint32_t bytes = (whole ? FL_A : FL_A / 2) + (S::BF16 && !up ? 2 : 1) * FL_B;
+                // the next unit is claimed a few stages before it is needed, so that the CTAs end together
+                const int claim_at = max(0, k_stages - 4);
+                int k = fl_first(e, blk, k_stages);
+                for (int ks = 0; ks < k_stages; ++ks) {
+                    if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, ctx, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&full[stage]);
+                    mbar_arrive_expect_tx(fb, bytes);
+                    tma_load_2d(smem_u32(smem + (size_t)stage * S::kStage), map, fb, x0 + k * FL_KB, y, policy);
+                    if (++k == k_stages) k = 0;
+                    if (++stage == NS) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (ks == claim_at) claim = atomicAdd(a.counters, 1);
+                }
             }
-            const int e = lst_e[pr.i], one_less = a.share.rows - n;   // 0 or 1
-            // chunk j of the shared expert: columns from j F on (past j's end: the next chunk's weights,
-            // which meet activations of zero)
-            if (e < a.E)
-                put.fill(&maps.down[one_less], pr.k * a.down.chunk, e * a.H + y, n * a.down.chunk, policy);
-            else
-                put.fill(&maps.down_s[one_less], (e - a.E) * a.F * ES + pr.k * a.down.chunk, y, n * a.down.chunk, policy);
-            pr.step(lst_e, n_list, a.down.n, w);
-            return pr.i < n_list || next_unit();
-        };
-        if (!fw_produce(put, active, step, ctx, abort_flag)) fw_settle();
-        return;
+            if (!ok) settle();
+        }
+    } else if (warp == 6) {
+        // ---------------------------------------------------------------- the units' columns: tokens or h
+        // A thread of its own: the weights of a down unit load while this one waits for its entry.
+        if (lane == 0) {
+            const uint64_t policy = l2_policy_evict_last();
+            int stage = 0, qs = 0, u;
+            uint32_t phase = 0, qph = 0;
+            bool ok = true;
+            while (ok && next_unit(qs, qph, u)) {
+                const bool up = u < n_up;
+                const int v = up ? u : u - n_up, mb = up ? a.m_up : a.m_down;
+                const int i = v / mb, blk = v - i * mb, k_stages = up ? a.k_up : a.k_down;
+                const int y = up ? 0 : lst_off[i];
+                const CUtensorMap* map = up ? &maps.x : &maps.h;
+                if (!up) {
+                    ok = wait_count(done + i, 4 * a.m_up, ctx, abort_flag);
+                    if (!ok) break;
+                    fence_proxy_async_global();
+                }
+                int k = fl_first(lst_e[i], blk, k_stages);
+                for (int ks = 0; ks < k_stages; ++ks) {
+                    if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, ctx, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&full[stage]), dst = smem_u32(smem + (size_t)stage * S::kStage) + FL_A;
+                    tma_load_2d(dst, map, fb, k * FL_KB, y, policy);
+                    if (S::BF16 && !up) tma_load_2d(dst + FL_B, map, fb, k * FL_KB, rows + y, policy);
+                    if (++k == k_stages) k = 0;
+                    if (++stage == NS) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok || *abort_flag) settle();
+        }
+    } else if (warp == 1 || warp == 7) {
+        // ---------------------------------------------------------------- products
+        // The issue of a stage's four instructions takes one thread about as long as the stage's share
+        // of HBM: two threads take turns.
+        if (lane == 0) {
+            const int m = warp == 7;
+            int stage = 0, qs = 0, slot = 0, u;
+            uint32_t phase = 0, qph = 0, sph = 0;
+            bool ok = true, issued = false;
+            while (ok && next_unit(qs, qph, u)) {
+                const bool up = u < n_up;
+                const int k_stages = up ? a.k_up : a.k_down;
+                const uint32_t idesc = make_idesc(S::BF16 ? 1u : 0u, FL_BM, S::BF16 && !up ? 2 * FL_N : FL_N);
+                if (!S::BLOCK && !mbar_wait(smem_u32(&rempty[slot]), sph ^ 1u, ctx, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                for (int ks = 0; ks < k_stages; ++ks) {
+                    if (ks % FL_MMA == m) {
+                        if (!mbar_wait(smem_u32(&full[stage]), phase, ctx, abort_flag) ||
+                            (S::BLOCK && !mbar_wait(smem_u32(&rempty[slot]), sph ^ 1u, ctx, abort_flag))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t wa = smem_u32(smem + (size_t)stage * S::kStage);
+                        const uint64_t wd = sw128_desc(wa), bd = sw128_desc(wa + FL_A);
+                        const uint32_t d = tmem_base + (uint32_t)((slot * S::kSums + (S::BLOCK ? 0 : 2 * m)) * S::kCols);
+                        const uint32_t first = S::BLOCK || ks < FL_MMA ? 0u : 1u;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)   // 32 bytes of K each (the descriptors count 16)
+                            mma_ss<!S::BF16>(d + (kk % 2) * S::kCols, wd + 2 * kk, bd + 2 * kk, idesc,
+                                             kk >= 2 ? 1u : first);
+                        issued = true;
+                        mma_commit(smem_u32(&empty[stage]));
+                        if (S::BLOCK) mma_commit(smem_u32(&rfull[slot]));
+                    }
+                    if (++stage == NS) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (S::BLOCK || ks == k_stages - 1) {
+                        if (!S::BLOCK) mma_commit(smem_u32(&rfull[slot]));
+                        if (++slot == S::kSlots) {
+                            slot = 0;
+                            sph ^= 1u;
+                        }
+                    }
+                }
+            }
+            if ((!ok || *abort_flag) && issued) {   // every MMA issued so far ends before TMEM is released
+                mma_commit(smem_u32(drain + m));
+                mbar_wait_drain(smem_u32(drain + m), 0, ctx.timeout_ns);
+            }
+        }
+    } else if (warp >= 2 && warp < 6) {
+        // ---------------------------------------------------------------- epilogue: a lane per weight row
+        const int q = warp & 3;   // TMEM lanes 32 q ..
+        const uint32_t t_lane = tmem_base + ((uint32_t)(q * 32) << 16);
+        int qs = 0, slot = 0;
+        uint32_t qph = 0, sph = 0;
+        bool ok = true;
+        while (ok) {
+            if (!mbar_wait_warp(smem_u32(&uq_full[qs]), qph, ctx, abort_flag)) break;
+            const int u = uq[qs];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&uq_empty[qs]));
+            if (++qs == FL_UQ) {
+                qs = 0;
+                qph ^= 1u;
+            }
+            if (u < 0) break;
+            const bool up = u < n_up;
+            const int v = up ? u : u - n_up, mb = up ? a.m_up : a.m_down;
+            const int i = v / mb, blk = v - i * mb, e = lst_e[i], n_out = up ? a.F : a.H;
+            const int row = blk * FL_BM + q * 32 + lane;
+            const bool in = row < n_out;
+            float z[FL_N];
+            if constexpr (S::BLOCK) {
+                const int kb = up ? a.k_up : a.k_down;
+                const float* ws = (up ? a.su : a.sd) + ((int64_t)e * n_out + (in ? row : 0)) * kb;
+#pragma unroll
+                for (int c = 0; c < FL_N; ++c) z[c] = 0.0f;
+                int b = fl_first(e, blk, kb);
+                float sw = __ldg(ws + b);
+                for (int ks = 0; ks < kb; ++ks) {
+                    if (++b == kb) b = 0;
+                    const float next = __ldg(ws + b);
+                    if (!mbar_wait_warp(smem_u32(&rfull[slot]), sph, ctx, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    float p[FL_N];
+                    fl_read<FMT>(t_lane + (uint32_t)(slot * S::kSums * S::kCols), false, false, p);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&rempty[slot]));
+                    if (++slot == S::kSlots) {
+                        slot = 0;
+                        sph ^= 1u;
+                    }
+#pragma unroll
+                    for (int c = 0; c < FL_N; ++c) z[c] = __fmaf_rn(sw, p[c], z[c]);
+                    sw = next;
+                }
+                if (!ok) break;
+            } else {
+                if (!mbar_wait_warp(smem_u32(&rfull[slot]), sph, ctx, abort_flag)) break;
+                tc_fence_after();
+                fl_read<FMT>(t_lane + (uint32_t)(slot * S::kSums * S::kCols), !up, (up ? a.k_up : a.k_down) == 1, z);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&rempty[slot]));
+                if (++slot == S::kSlots) {
+                    slot = 0;
+                    sph ^= 1u;
+                }
+            }
+            const int mask = lst_mask[i];
+            if (up) {
+                // columns are tokens; the entry's keep their order in its rows of h
+                const float sc = S::BF16 ? 1.0f : S::BLOCK ? a.x_scale : __fmul_rn(a.su[e], a.x_scale);
+                const int64_t o0 = (int64_t)lst_off[i] * a.F + row;
+                int c = 0;
+#pragma unroll
+                for (int t = 0; t < FL_N; ++t) {
+                    if (!((mask >> t) & 1)) continue;
+                    const int64_t o = o0 + (int64_t)c * a.F;
+                    ++c;
+                    if (!in) continue;
+                    float zz = z[t];
+                    if constexpr (!S::BF16) zz = __fmul_rn(zz, sc);
+                    const float h = zz <= 0.0f ? 0.0f : __fmul_rn(zz, zz);   // a NaN stays one
+                    if constexpr (S::BF16) {
+                        // h as the sum of two bf16, 16 bits of it: one alone would add a second rounding
+                        // of the output's size
+                        const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+                        const float top = __bfloat162float(hi);
+                        __nv_bfloat16* hp = reinterpret_cast<__nv_bfloat16*>(a.h) + o;
+                        hp[0] = hi;
+                        hp[(int64_t)rows * a.F] =
+                            __float2bfloat16_rn(top < __uint_as_float(0x7f800000u) ? __fsub_rn(h, top) : 0.0f);
+                    } else {
+                        a.h[o] = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(h, a.h_scale), __NV_SATFINITE, __NV_E4M3);
+                    }
+                }
+                // for the TMA loads of h: every lane's stores, then the warp's report
+                fence_proxy_async_global();
+                __syncwarp();
+                if (lane == 0 && !(a.hold && u == 0)) red_release_add(done + i, 1);
+            } else {
+                const float sc = S::BF16 ? 1.0f : S::BLOCK ? a.h_scale : __fmul_rn(a.sd[e], a.h_scale);
+                const int n_tok = __popc(mask);
+#pragma unroll
+                for (int c = 0; c < FL_N; ++c)
+                    if (c < n_tok && in) {
+                        float y = z[c];
+                        if constexpr (!S::BF16) y = __fmul_rn(y, sc);
+                        __stcg(a.y + (int64_t)rowi[i * 16 + c] * a.H + row, y);
+                    }
+                // the last entry's warp for these 32 rows sums them
+                __syncwarp();
+                int last = 0;
+                if (lane == 0) {
+                    __threadfence();
+                    last = atomicAdd(summed + blk * 4 + q, 1) == n_list - 1;
+                    __threadfence();
+                }
+                if (__shfl_sync(0xffffffffu, last, 0) && in) {
+                    // every token's term k at once: the reads of L2 are what this takes
+                    float o[FL_N] = {};
+#pragma unroll 2
+                    for (int k = 0; k < a.K; ++k) {
+                        const float* y = a.y + (int64_t)k * a.H + row;
+#pragma unroll
+                        for (int t = 0; t < FL_N; ++t)
+                            if (t < a.T) o[t] = __fmaf_rn(sel_w[t][k], __ldcg(y + (int64_t)t * a.K * a.H), o[t]);
+                    }
+                    for (int j = 0; j < a.ns; ++j) {
+                        const float* y = a.y + (int64_t)a.T * (a.K + j) * a.H + row;
+#pragma unroll
+                        for (int t = 0; t < FL_N; ++t)
+                            if (t < a.T) o[t] = __fadd_rn(o[t], __ldcg(y + (int64_t)t * a.H));
+                    }
+#pragma unroll
+                    for (int t = 0; t < FL_N; ++t)
+                        if (t < a.T) {
+                            const int64_t at = (int64_t)t * a.H + row;
+                            if (a.residual) o[t] = __fadd_rn(o[t], bf16_bits_to_float(a.residual[at]));
+                            a.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(o[t]));
+                        }
+                }
+                __syncwarp();
+            }
+        }
     }
 
-    // ---- consumers: pieces
-    fw_consumer_regs();
-    FwTake ring(rings, warp);
-    while (true) {
-        if (!ring.wait(ctx, abort_flag)) return fw_settle();
-        const int piece = slot_piece[warp * FW_MAX_STAGES + ring.slot];
-        if (piece >= n_pieces) {
-            ring.release();
-            break;
-        }
-        const int i = piece / per, f = (piece - i * per) * FEW_PIECE;
-        const int n_tok = lst_n[i];
-        const bool ok = n_tok <= 8
-                            ? few_up<FMT, 1>(a, ring, lst_e[i], f, n_tok, rowi + i * 16, tok + i * 16, ctx, abort_flag)
-                            : few_up<FMT, 2>(a, ring, lst_e[i], f, n_tok, rowi + i * 16, tok + i * 16, ctx, abort_flag);
-        if (!ok) return fw_settle();
-        __syncwarp();
-        if (lane == 0 && !(a.hold && piece == 0)) {
-            __threadfence();
-            red_release_add(a.counters + 1, 1);
-        }
-    }
-
-    // ---- output rows, once every piece has reported
-    {
-        int good = 1;
-        if (lane == 0) good = wait_count(a.counters + 1, n_pieces, ctx, abort_flag) ? 1 : 0;
-        if (!__shfl_sync(0xffffffffu, good, 0)) return fw_settle();
-        __syncwarp();
-    }
-    for (int un = 0; un < a.share.units; ++un) {
-        const int u = blockIdx.x * a.share.units + un;
-        const int d0 = unit_row(u), n = unit_row(u + 1) - d0;
-        float* tot = red.mine(warp);
-        for (int j = lane; j < FwRed::kWarp; j += 32) tot[j] = 0.0f;
-        __syncwarp();
-        if (n > 0) {
-            FewDown<FMT> down{a, ring, lst_e, lst_n, rowi, tok, wt, n_list, warp, d0, n, tot, ctx, abort_flag};
-            if (!down.run()) return fw_settle();
-        }
-        if (!red.exchange(ctx, abort_flag)) return fw_settle();
-        for (int j = tid; j < n * a.T; j += 32 * FW_WARPS) {
-            const int t = j / n, row = j - t * n;
-            float o = red.sum(t, row);
-            if constexpr (FMT != MOE_BF16) o = __fmul_rn(o, a.h_scale);
-            const int64_t at = (int64_t)t * a.H + d0 + row;
-            if (a.residual) o = __fadd_rn(o, bf16_bits_to_float(a.residual[at]));
-            a.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
-        }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, S::kTmem);
     }
 }
 
 // ----------------------------------------------------------------------------- host
 
-static int few_row_bytes(int K, int dtype) { return dtype == MOE_BF16 ? 2 * K : dtype == MOE_FP8_B128 ? (K + 127) / 128 * 128 : K; }
-
-typedef CUresult (*FwEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static FwEncodeFn fw_encode_fn() {
-    static const FwEncodeFn fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-                        q == cudaDriverEntryPointSuccess;
-        return ok ? reinterpret_cast<FwEncodeFn>(p) : nullptr;
-    }();
-    return fn;
+static int few_row_bytes(int K, int dtype) {
+    return dtype == MOE_BF16 ? 2 * K : dtype == MOE_FP8_B128 ? (K + 127) / 128 * 128 : K;
 }
 
-bool fw_map(CUtensorMap* m, const void* base, int64_t rows, int64_t bytes, int64_t ld, int chunk, int box_rows) {
-    const FwEncodeFn fn = fw_encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)bytes / 4, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld};
-    const cuuint32_t box[2] = {(cuuint32_t)chunk / 4, (cuuint32_t)box_rows}, estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+int few_counters(const moe_dims* d) {
+    const int64_t n_list = std::min<int64_t>(d->E, d->T * d->K) + d->Fs / d->F;
+    return (int)(1 + n_list + 4 * ((d->H + FL_BM - 1) / FL_BM));
 }
 
 template <int FMT>
 static cudaError_t launch_layer(const FewMaps& maps, FewArgs& a, int num_sms, const DevCtx& ctx, cudaStream_t stream) {
-    const size_t fixed = FwRed::bytes(a.share.units) + few_table_bytes(a.n_list_max);
-    a.n_stages = (int)std::min<size_t>(FW_MAX_STAGES, (FW_SMEM - fixed) / FW_WARPS / a.slot_bytes);
-    const size_t smem = (size_t)FW_WARPS * a.n_stages * a.slot_bytes + fixed;
+    using S = FlShape<FMT>;
+    const size_t fixed = 1024 + few_table_bytes(a.n_list_max);
+    a.n_stages = (int)std::min<size_t>(FL_MAX_STAGES, (FL_SMEM - fixed) / S::kStage);
+    const size_t smem = (size_t)a.n_stages * S::kStage + fixed;
     auto k = few_layer_kernel<FMT>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_k(k, dim3(num_sms), dim3(FW_THREADS), smem, stream, maps, a, ctx);
+    const int64_t units = (int64_t)a.n_list_max * (a.m_up + a.m_down);
+    return launch_k(k, dim3((unsigned)std::min<int64_t>(units, num_sms)), dim3(FL_THREADS), smem, stream, maps, a, ctx);
 }
 
 cudaError_t launch_few(const moe_dims* d, const uint16_t* x, const uint16_t* wr, const float* bias, const void* w_up,
@@ -696,60 +752,68 @@ cudaError_t launch_few(const moe_dims* d, const uint16_t* x, const uint16_t* wr,
                        const uint16_t* residual, uint16_t* out, int32_t* idx, float* w, const FewWs& ws, int hold,
                        int num_sms, const DevCtx& ctx, cudaStream_t stream) {
     const bool fp8 = d->expert_dtype != MOE_BF16;
-    FewRouterArgs r = {};
-    r.x = x;
-    r.wr = wr;
-    r.bias = bias;
-    r.T = (int)d->T;
-    r.H = d->H;
-    r.E = d->E;
-    r.logits = ws.logits;
-    r.xq = fp8 ? reinterpret_cast<__half*>(ws.xq) : nullptr;
-    r.x_scale = fp8 ? sc->x_scale : 1.0f;
-    r.counters = ws.counters;
-    cudaError_t e = launch_k(few_router_kernel, dim3(d->E + (fp8 ? r.T : 0)), dim3(FEW_RT), 0, stream, r, ctx);
-    if (e != cudaSuccess) return e;
-
+    const int T = (int)d->T, ns = d->Fs / d->F, rows = T * (d->K + ns);
     FewArgs a = {};
-    a.x = x;
     a.residual = residual;
     a.out = out;
     a.topk_idx = idx;
     a.topk_w = w;
     a.logits = ws.logits;
-    a.act = fp8 ? ws.xq : reinterpret_cast<const uint8_t*>(x);
-    a.first = std::min((d->K + d->Fs / d->F) * (d->F / FEW_PIECE) / num_sms, FW_WARPS);
     a.su = fp8 ? sc->w_up_scale : nullptr;
     a.sd = fp8 ? sc->w_down_scale : nullptr;
     a.x_scale = fp8 ? sc->x_scale : 1.0f;
     a.h_scale = fp8 ? sc->h_scale : 1.0f;
-    a.ns = d->Fs / d->F;
     a.h = ws.h;
-    a.h_lo = d->T * (int64_t)(d->K + a.ns) * d->F * 2;
+    a.y = ws.y;
     a.counters = ws.counters;
-    a.T = r.T;
+    a.T = T;
     a.H = d->H;
     a.E = d->E;
     a.K = d->K;
     a.F = d->F;
-    const bool block = d->expert_dtype == MOE_FP8_B128;
-    a.up = fw_cut(few_row_bytes(d->H, d->expert_dtype), block);
-    a.down = fw_cut(few_row_bytes(d->F, d->expert_dtype), block);
-    a.share = fw_share(d->H, num_sms);
-    a.slot_bytes = (std::max(a.share.rows, FEW_PIECE) * a.up.chunk + 127) / 128 * 128;
-    FewMaps maps = {};
-    const int ns = a.ns;
-    bool ok = fw_map(&maps.up, w_up, (int64_t)d->E * d->F, a.up.bytes, a.up.bytes, a.up.chunk, FEW_PIECE);
-    if (ns > 0) ok = ok && fw_map(&maps.up_s, w_up_s, (int64_t)ns * d->F, a.up.bytes, a.up.bytes, a.up.chunk, FEW_PIECE);
-    for (int i = 0; i < 2 && a.share.rows > i; ++i)
-        ok = ok && fw_map(&maps.down[i], w_down, (int64_t)d->E * d->H, a.down.bytes, a.down.bytes, a.down.chunk,
-                          a.share.rows - i);
-    for (int i = 0; i < 2 && ns > 0 && a.share.rows > i; ++i)
-        ok = ok && fw_map(&maps.down_s[i], w_down_s, d->H, (int64_t)d->Fs * 2, (int64_t)d->Fs * 2, a.down.chunk,
-                          a.share.rows - i);
-    if (!ok) return cudaErrorInvalidValue;
-    a.n_list_max = (int)std::min<int64_t>(d->E, d->T * d->K) + a.ns;
+    a.ns = ns;
+    a.m_up = (d->F + FL_BM - 1) / FL_BM;
+    a.m_down = (d->H + FL_BM - 1) / FL_BM;
+    a.n_list_max = (int)std::min<int64_t>(d->E, d->T * d->K) + ns;
     a.hold = hold;
+    const int ub = few_row_bytes(d->H, d->expert_dtype), db = few_row_bytes(d->F, d->expert_dtype);
+    const int es = fp8 ? 1 : 2;
+    a.k_up = (ub + FL_KB - 1) / FL_KB;
+    a.k_down = (db + FL_KB - 1) / FL_KB;
+    FewMaps maps = {};
+    const int64_t ur = (int64_t)d->E * d->F, dr = (int64_t)d->E * d->H;
+    // a box of 64 rows serves the last rows of an expert when 64 or fewer are left
+    const bool u64 = d->F % FL_BM > 0 && d->F % FL_BM <= 64, d64 = d->H % FL_BM > 0 && d->H % FL_BM <= 64;
+    bool ok = make_map_u8_b128(&maps.up128, w_up, ur, ub, 128) && make_map_u8_b128(&maps.down128, w_down, dr, db, 128) &&
+              make_map_u8_b128(&maps.x, fp8 ? static_cast<const void*>(ws.xq) : x, T, (int64_t)d->H * es, FL_N) &&
+              make_map_u8_b128(&maps.h, ws.h, (int64_t)rows * es, (int64_t)d->F * es, FL_N);
+    if (u64) ok = ok && make_map_u8_b128(&maps.up64, w_up, ur, ub, 64);
+    if (d64) ok = ok && make_map_u8_b128(&maps.down64, w_down, dr, db, 64);
+    if (ns > 0) {
+        ok = ok && make_map_u8_b128(&maps.ups128, w_up_s, d->Fs, ub, 128) &&
+             make_map_u8_b128(&maps.downs128, w_down_s, d->H, (int64_t)d->Fs * 2, 128);
+        if (u64) ok = ok && make_map_u8_b128(&maps.ups64, w_up_s, d->Fs, ub, 64);
+        if (d64) ok = ok && make_map_u8_b128(&maps.downs64, w_down_s, d->H, (int64_t)d->Fs * 2, 64);
+        a.warm[0] = static_cast<const uint8_t*>(w_up_s);
+        a.warm[1] = static_cast<const uint8_t*>(w_down_s);
+        a.warm_bytes = std::min<int64_t>((int64_t)d->Fs * d->H * 2, kFewWarmBytes);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+
+    FewRouterArgs r = {};
+    r.x = x;
+    r.wr = wr;
+    r.bias = bias;
+    r.T = T;
+    r.H = d->H;
+    r.E = d->E;
+    r.logits = ws.logits;
+    r.xq = fp8 ? ws.xq : nullptr;
+    r.x_scale = a.x_scale;
+    r.counters = ws.counters;
+    r.n_counters = few_counters(d);
+    const cudaError_t e = launch_k(few_router_kernel, dim3(d->E + (fp8 ? T : 0)), dim3(FEW_RT), 0, stream, r, ctx);
+    if (e != cudaSuccess) return e;
     switch (d->expert_dtype) {
         case MOE_BF16: return launch_layer<MOE_BF16>(maps, a, num_sms, ctx, stream);
         case MOE_FP8_E4M3: return launch_layer<MOE_FP8_E4M3>(maps, a, num_sms, ctx, stream);

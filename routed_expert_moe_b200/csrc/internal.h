@@ -113,15 +113,16 @@ cudaError_t launch_quantize(int64_t n_tensors, int64_t elems, const uint16_t* sr
 cudaError_t launch_ep_regroup(const int64_t* recv_counts, int W, int E_loc, int64_t R, int32_t* offsets,
                               int32_t* perm, int32_t* inv, const DevCtx& ctx, cudaStream_t stream);
 
-// The few-token layer (few.cu): at most this many tokens, two columns' worth of the 8-column
-// matrix instruction.
+// The few-token layer (few.cu): at most this many tokens, the columns of its matrix instructions.
 constexpr int kFewMaxTokens = 16;
 struct FewWs {
-    int* counters;        // [2]: unit claims, up reports
+    int* counters;        // [few_counters]
     long long* logits;    // [T][E]
-    uint8_t* xq;          // fp16 values of x's E4M3 codes [T][H] (quantised experts)
-    uint8_t* h;           // ReLU^2 rows [T*(K+ns)][F]: fp16 values of codes, or bf16 high parts, then low parts
+    uint8_t* xq;          // E4M3 codes of x [T][H] (quantised experts)
+    uint8_t* h;           // ReLU^2 rows [T*(K+ns)][F]: E4M3 codes, or bf16 high parts and then low parts
+    float* y;             // expert outputs [T*(K+ns)][H]
 };
+int few_counters(const moe_dims* d);
 cudaError_t launch_few(const moe_dims* d, const uint16_t* x, const uint16_t* wr, const float* bias, const void* w_up,
                        const void* w_down, const void* w_up_s, const void* w_down_s, const moe_fp8_scales* sc,
                        const uint16_t* residual, uint16_t* out, int32_t* idx, float* w, const FewWs& ws, int hold,

@@ -47,7 +47,7 @@ def test_workspace_covers_the_few_token_layer(moe):
     for T, H, E, K, F in [(16, 16, 256, 1, 16), (1, 16, 256, 1, 16), (16, 2688, 128, 6, 1856), (16, 16, 16, 16, 65536)]:
         for kw in ({}, dict(fp8=True), dict(fp8_b128=True)):
             fp8 = bool(kw)
-            need = 8 * T * E + (2 * T * H if fp8 else 0) + T * K * F * (2 if fp8 else 4)
+            need = 8 * T * E + (T * H if fp8 else 0) + T * K * F * (1 if fp8 else 4) + 4 * T * K * H
             assert moe.workspace_size(moe.dims(T, H, E, K, F, **kw)) >= need
 
 
