@@ -38,7 +38,8 @@
 
 namespace moe {
 
-constexpr int FEW_RT = 256;          // threads of the router kernel
+constexpr int FEW_RT = 512;          // threads of the router kernel
+constexpr int FEW_RW = FEW_RT / 32;
 
 // ----------------------------------------------------------------------------- router
 
@@ -56,8 +57,8 @@ struct FewRouterArgs {
 
 __global__ void __launch_bounds__(FEW_RT) few_router_kernel(FewRouterArgs a, DevCtx ctx) {
     pdl_enter();
-    __shared__ long long s_l[kFewMaxTokens][8];
-    __shared__ float s_x[kFewMaxTokens][8], s_w[8];
+    __shared__ long long s_l[kFewMaxTokens][FEW_RW];
+    __shared__ float s_x[kFewMaxTokens][FEW_RW], s_w[FEW_RW];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int nv = a.H / 8;
     if ((int)blockIdx.x >= a.E) {   // one token's E4M3 codes
@@ -80,24 +81,62 @@ __global__ void __launch_bounds__(FEW_RT) few_router_kernel(FewRouterArgs a, Dev
     const int e = blockIdx.x;
     for (int i = e * FEW_RT + tid; i < a.n_counters; i += a.E * FEW_RT) a.counters[i] = 0;
     // a warp takes one token over 1 / parts of H
-    const int parts = a.T == 1 ? 8 : a.T == 2 ? 4 : a.T <= 4 ? 2 : 1;
-    const int part = warp % parts;
+    const int parts = a.T == 1 ? 16 : a.T == 2 ? 8 : a.T <= 4 ? 4 : a.T <= 8 ? 2 : 1;
+    const int part = warp % parts, t = warp / parts;
     const uint4* wv = reinterpret_cast<const uint4*>(a.wr + (int64_t)e * a.H);
-    for (int t = warp / parts; t < a.T; t += 8 / parts) {
+    if (t < a.T) {
         const uint4* xv = reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.H);
         long long acc = 0;
-        float xs = 0.0f, ws = 0.0f;
-#pragma unroll 4
-        for (int v = part * 32 + lane; v < nv; v += 32 * parts) {
-            const uint4 p = xv[v], r = wv[v];
-            const uint32_t pp[4] = {p.x, p.y, p.z, p.w}, rr[4] = {r.x, r.y, r.z, r.w};
+        float xs = 0.0f, ws = 0.0f, big = 0.0f;
+        // A product p, |p| < 32, as two integers by fp32 additions alone (a conversion to 64 bits takes
+        // 16 times as long): adding kHi rounds it to the grid 2^-17, what is left over is exact and at
+        // most 2^-18, and adding kLo rounds that to the grid 2^-40, ties to even like the sum of both,
+        // since the first part is an even multiple of 2^-40.  The bits of the two sums count grid steps
+        // from those of the constants.
+        constexpr float kHi = 96.0f, kLo = 1.5f * 0x1p-17f;
+        constexpr int B = 4;   // vectors whose loads are under way together
+        for (int v0 = part * 32 + lane; v0 < nv; v0 += 32 * parts * B) {
+            uint4 pv[B], rv[B];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float f = __uint_as_float((j & 1) ? (pp[j / 2] & 0xFFFF0000u) : (pp[j / 2] << 16));
-                const float h = __uint_as_float((j & 1) ? (rr[j / 2] & 0xFFFF0000u) : (rr[j / 2] << 16));
-                acc += __float2ll_rn(__fmul_rn(__fmul_rn(f, h), 0x1p40f));   // the product is exact
-                xs = __fmaf_rn(f, f, xs);
-                ws = __fmaf_rn(h, h, ws);
+            for (int b = 0; b < B; ++b) {
+                const int v = v0 + 32 * parts * b;
+                pv[b] = rv[b] = make_uint4(0, 0, 0, 0);
+                if (v < nv) {
+                    pv[b] = xv[v];
+                    rv[b] = wv[v];
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const uint32_t pp[4] = {pv[b].x, pv[b].y, pv[b].z, pv[b].w}, rr[4] = {rv[b].x, rv[b].y, rv[b].z, rv[b].w};
+                uint32_t n_hi = 0, n_lo = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float f = __uint_as_float((j & 1) ? (pp[j / 2] & 0xFFFF0000u) : (pp[j / 2] << 16));
+                    const float h = __uint_as_float((j & 1) ? (rr[j / 2] & 0xFFFF0000u) : (rr[j / 2] << 16));
+                    const float p = __fmul_rn(f, h);   // exact
+                    const float hi = __fadd_rn(p, kHi);
+                    const float lo = __fadd_rn(__fsub_rn(p, __fsub_rn(hi, kHi)), kLo);
+                    n_hi += __float_as_uint(hi);
+                    n_lo += __float_as_uint(lo);
+                    big = fmaxf(big, fabsf(p));
+                    xs = __fmaf_rn(f, f, xs);
+                    ws = __fmaf_rn(h, h, ws);
+                }
+                acc += ((long long)(int)(n_hi - 8u * __float_as_uint(kHi)) << 23) + (int)(n_lo - 8u * __float_as_uint(kLo));
+            }
+        }
+        if (!__all_sync(0xffffffffu, big < 32.0f && xs < 3.0e38f && ws < 3.0e38f)) {
+            // a product outside the range of the two roundings above
+            acc = 0;
+            for (int v = part * 32 + lane; v < nv; v += 32 * parts) {
+                const uint4 p4 = xv[v], r4 = wv[v];
+                const uint32_t pp[4] = {p4.x, p4.y, p4.z, p4.w}, rr[4] = {r4.x, r4.y, r4.z, r4.w};
+                for (int j = 0; j < 8; ++j) {
+                    const float f = __uint_as_float((j & 1) ? (pp[j / 2] & 0xFFFF0000u) : (pp[j / 2] << 16));
+                    const float h = __uint_as_float((j & 1) ? (rr[j / 2] & 0xFFFF0000u) : (rr[j / 2] << 16));
+                    acc += __float2ll_rn(__fmul_rn(__fmul_rn(f, h), 0x1p40f));
+                }
             }
         }
 #pragma unroll
@@ -133,7 +172,7 @@ __global__ void __launch_bounds__(FEW_RT) few_router_kernel(FewRouterArgs a, Dev
 
 // ----------------------------------------------------------------------------- layer
 
-constexpr int FL_THREADS = 512;     // weights, two of products, four of the epilogue, columns; all route
+constexpr int FL_THREADS = 384;     // weights, two of products, four of the epilogue, columns; all route
 constexpr int FL_MMA = 2;           // warps that issue products: of the even and of the odd stages
 constexpr int FL_BM = 128;          // weight rows per unit
 constexpr int FL_KB = 128;          // bytes of K per stage (E4M3: one scale block)
@@ -275,6 +314,57 @@ __device__ __forceinline__ void fl_read(uint32_t addr, bool down, bool one, floa
     }
 }
 
+// out[t][r .. r + 3] for t = t0, t0 + 4, ..: the weighted sum over the experts in the order of the token's
+// choice, the shared chunks, the residual, one rounding.  What this takes is reads of L2 one after the
+// other, so eight terms of two tokens are under way together.
+__device__ __forceinline__ void fl_combine(const FewArgs& a, const float (*sel_w)[16], int r, int t0) {
+    if (r >= a.H) return;   // H is a multiple of 16
+    constexpr int KB = 8;
+    const int terms = a.K + a.ns;
+    for (; t0 < a.T; t0 += 8) {
+        float4 o[2] = {};
+        for (int k0 = 0; k0 < terms; k0 += KB) {
+            float4 v[2][KB];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < KB; ++j) {
+                    const int t = t0 + 4 * i, k = k0 + j;
+                    const int64_t row = k < a.K ? (int64_t)t * a.K + k : (int64_t)a.T * k + t;
+                    if (t < a.T && k < terms) v[i][j] = __ldcg(reinterpret_cast<const float4*>(a.y + row * a.H + r));
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < KB; ++j) {
+                    const int t = t0 + 4 * i, k = k0 + j;
+                    if (t >= a.T || k >= terms) continue;
+                    const float w = k < a.K ? sel_w[t][k] : 1.0f;
+                    o[i].x = __fmaf_rn(w, v[i][j].x, o[i].x);
+                    o[i].y = __fmaf_rn(w, v[i][j].y, o[i].y);
+                    o[i].z = __fmaf_rn(w, v[i][j].z, o[i].z);
+                    o[i].w = __fmaf_rn(w, v[i][j].w, o[i].w);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = t0 + 4 * i;
+            if (t >= a.T) continue;
+            const int64_t at = (int64_t)t * a.H + r;
+            if (a.residual) {
+                const uint2 s = *reinterpret_cast<const uint2*>(a.residual + at);
+                o[i].x = __fadd_rn(o[i].x, __uint_as_float(s.x << 16));
+                o[i].y = __fadd_rn(o[i].y, __uint_as_float(s.x & 0xFFFF0000u));
+                o[i].z = __fadd_rn(o[i].z, __uint_as_float(s.y << 16));
+                o[i].w = __fadd_rn(o[i].w, __uint_as_float(s.y & 0xFFFF0000u));
+            }
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(o[i].x, o[i].y), hi = __floats2bfloat162_rn(o[i].z, o[i].w);
+            *reinterpret_cast<uint2*>(a.out + at) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+    }
+}
+
 // The stage of K that a unit begins with.  Every CTA reads the same columns (x, or one entry's rows of
 // h): in step, all of them would ask one L2 slice for the same lines.  It goes by expert and block alone,
 // so that a row's sum does not hang on the batch.
@@ -347,18 +437,18 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
     const uint32_t tmem_base = *tmem_holder;
     pdl_enter();
 
-    // ---- the routing, the same in every CTA: one warp per token
-    if (warp < a.T) {
+    // ---- the routing, the same in every CTA: a warp per token
+    for (int t = warp; t < a.T; t += FL_THREADS / 32) {
         int e;
         float w;
-        few_select(a.logits + (int64_t)warp * a.E, a.E, a.K, lane, e, w);
+        few_select(a.logits + (int64_t)t * a.E, a.E, a.K, lane, e, w);
         if (lane < a.K) {
-            sel_e[warp][lane] = e;
-            sel_w[warp][lane] = w;
-            atomicOr(&emask[e], 1 << warp);
+            sel_e[t][lane] = e;
+            sel_w[t][lane] = w;
+            atomicOr(&emask[e], 1 << t);
             if (blockIdx.x == 0) {
-                if (a.topk_idx) a.topk_idx[warp * a.K + lane] = e;
-                if (a.topk_w) a.topk_w[warp * a.K + lane] = w;
+                if (a.topk_idx) a.topk_idx[t * a.K + lane] = e;
+                if (a.topk_w) a.topk_w[t * a.K + lane] = w;
             }
         }
     }
@@ -686,30 +776,8 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
                     last = atomicAdd(summed + blk * 4 + q, 1) == n_list - 1;
                     __threadfence();
                 }
-                if (__shfl_sync(0xffffffffu, last, 0) && in) {
-                    // every token's term k at once: the reads of L2 are what this takes
-                    float o[FL_N] = {};
-#pragma unroll 2
-                    for (int k = 0; k < a.K; ++k) {
-                        const float* y = a.y + (int64_t)k * a.H + row;
-#pragma unroll
-                        for (int t = 0; t < FL_N; ++t)
-                            if (t < a.T) o[t] = __fmaf_rn(sel_w[t][k], __ldcg(y + (int64_t)t * a.K * a.H), o[t]);
-                    }
-                    for (int j = 0; j < a.ns; ++j) {
-                        const float* y = a.y + (int64_t)a.T * (a.K + j) * a.H + row;
-#pragma unroll
-                        for (int t = 0; t < FL_N; ++t)
-                            if (t < a.T) o[t] = __fadd_rn(o[t], __ldcg(y + (int64_t)t * a.H));
-                    }
-#pragma unroll
-                    for (int t = 0; t < FL_N; ++t)
-                        if (t < a.T) {
-                            const int64_t at = (int64_t)t * a.H + row;
-                            if (a.residual) o[t] = __fadd_rn(o[t], bf16_bits_to_float(a.residual[at]));
-                            a.out[at] = __bfloat16_as_ushort(__float2bfloat16_rn(o[t]));
-                        }
-                }
+                if (__shfl_sync(0xffffffffu, last, 0))
+                    fl_combine(a, sel_w, blk * FL_BM + q * 32 + lane % 8 * 4, lane / 8);
                 __syncwarp();
             }
         }
