@@ -195,8 +195,8 @@ struct FlShape {
     // columns each, the second 16 for the low parts of h.
     static constexpr int kCols = BF16 ? 2 * FL_N : FL_N;
     static constexpr int kSums = BLOCK ? 2 : 2 * FL_MMA;
-    static constexpr int kSlots = BLOCK ? 8 : 2;
-    static constexpr int kTmem = kSlots * kSums * kCols;
+    static constexpr int kSlots = BLOCK ? 8 : 1;   // of each set of epilogue warps
+    static constexpr int kTmem = 2 * kSlots * kSums * kCols;
 };
 
 // Weights in boxes of 128 and of 64 rows (the last rows of an expert), tokens and h in boxes of 16.
@@ -228,7 +228,7 @@ struct FewArgs {
 // shared memory after the ring: barriers | queue, flags | lst_e, lst_mask, lst_off [n] i32 | rowi [n][16] u16 |
 // emask, eslot [256] i32 | sel_w [16][16] f32 | sel_e [16][16] i32
 __host__ __device__ inline size_t few_table_bytes(int n_list) {
-    return (2 * FL_MAX_STAGES + 2 * 8 + FL_MMA + 2 * FL_UQ) * 8 + (FL_UQ + 4) * 4 + (size_t)n_list * (3 * 4 + 32) + 4 * 1024 + 16;
+    return (2 * FL_MAX_STAGES + 2 * 16 + FL_MMA + 2 * FL_UQ) * 8 + (FL_UQ + 4) * 4 + (size_t)n_list * (3 * 4 + 32) + 4 * 1024 + 16;
 }
 
 // The K best experts of one token (one warp): by logit, ties to the lower index; lane k returns the
@@ -381,8 +381,8 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)NS * S::kStage);
     uint64_t* empty = full + FL_MAX_STAGES;
     uint64_t* rfull = empty + FL_MAX_STAGES;   // TMEM results
-    uint64_t* rempty = rfull + 8;
-    uint64_t* drain = rempty + 8;
+    uint64_t* rempty = rfull + 16;
+    uint64_t* drain = rempty + 16;
     uint64_t* uq_full = drain + FL_MMA;
     uint64_t* uq_empty = uq_full + FL_UQ;
     volatile int* uq = reinterpret_cast<volatile int*>(uq_empty + FL_UQ);
@@ -404,14 +404,14 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
-        for (int p = 0; p < S::kSlots; ++p) {
+        for (int p = 0; p < 2 * S::kSlots; ++p) {
             mbar_init(smem_u32(&rfull[p]), S::BLOCK ? 1 : FL_MMA);
             mbar_init(smem_u32(&rempty[p]), 4);
         }
         for (int m = 0; m < FL_MMA; ++m) mbar_init(smem_u32(drain + m), 1);
         for (int q = 0; q < FL_UQ; ++q) {
             mbar_init(smem_u32(&uq_full[q]), 1);
-            mbar_init(smem_u32(&uq_empty[q]), 1 + FL_MMA + 4);   // columns, products, epilogue warps
+            mbar_init(smem_u32(&uq_empty[q]), 1 + FL_MMA + 8);   // columns, products, epilogue warps
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -613,10 +613,10 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
         // of HBM: two threads take turns.
         if (lane == 0) {
             const int m = warp == 7;
-            int stage = 0, qs = 0, slot = 0, u;
-            uint32_t phase = 0, qph = 0, sph = 0;
+            int stage = 0, qs = 0, slot = 0, other = S::kSlots, u;
+            uint32_t phase = 0, qph = 0, sph = 0, other_ph = 0;
             bool ok = true, issued = false;
-            while (ok && next_unit(qs, qph, u)) {
+            for (int end = S::kSlots; ok && next_unit(qs, qph, u); end = 3 * S::kSlots - end) {
                 const bool up = u < n_up;
                 const int k_stages = up ? a.k_up : a.k_down;
                 const uint32_t idesc = make_idesc(S::BF16 ? 1u : 0u, FL_BM, S::BF16 && !up ? 2 * FL_N : FL_N);
@@ -650,23 +650,34 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
                     }
                     if (S::BLOCK || ks == k_stages - 1) {
                         if (!S::BLOCK) mma_commit(smem_u32(&rfull[slot]));
-                        if (++slot == S::kSlots) {
-                            slot = 0;
+                        if (++slot == end) {
+                            slot = end - S::kSlots;
                             sph ^= 1u;
                         }
                     }
                 }
+                // the next unit is the other set's
+                const int s = slot;
+                slot = other;
+                other = s;
+                const uint32_t p = sph;
+                sph = other_ph;
+                other_ph = p;
             }
             if ((!ok || *abort_flag) && issued) {   // every MMA issued so far ends before TMEM is released
                 mma_commit(smem_u32(drain + m));
                 mbar_wait_drain(smem_u32(drain + m), 0, ctx.timeout_ns);
             }
         }
-    } else if (warp >= 2 && warp < 6) {
+    } else {
         // ---------------------------------------------------------------- epilogue: a lane per weight row
+        // Two sets of four warps take turns: the stores, fences and counters at a unit's end take about
+        // as long as the reads of its sums.
         const int q = warp & 3;   // TMEM lanes 32 q ..
+        const int set = warp >= 8, first_slot = set * S::kSlots;   // its own slots
+        bool mine = set;
         const uint32_t t_lane = tmem_base + ((uint32_t)(q * 32) << 16);
-        int qs = 0, slot = 0;
+        int qs = 0, slot = first_slot;
         uint32_t qph = 0, sph = 0;
         bool ok = true;
         while (ok) {
@@ -680,6 +691,8 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
             }
             if (u < 0) break;
             const bool up = u < n_up;
+            mine = !mine;
+            if (!mine) continue;
             const int v = up ? u : u - n_up, mb = up ? a.m_up : a.m_down;
             const int i = v / mb, blk = v - i * mb, e = lst_e[i], n_out = up ? a.F : a.H;
             const int row = blk * FL_BM + q * 32 + lane;
@@ -705,8 +718,8 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&rempty[slot]));
-                    if (++slot == S::kSlots) {
-                        slot = 0;
+                    if (++slot == first_slot + S::kSlots) {
+                        slot = first_slot;
                         sph ^= 1u;
                     }
 #pragma unroll
@@ -721,8 +734,8 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&rempty[slot]));
-                if (++slot == S::kSlots) {
-                    slot = 0;
+                if (++slot == first_slot + S::kSlots) {
+                    slot = first_slot;
                     sph ^= 1u;
                 }
             }
