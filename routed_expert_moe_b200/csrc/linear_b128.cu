@@ -160,8 +160,10 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
 constexpr int LT_BM = 128;              // rows of x per tile (TMEM lanes)
 constexpr int LT_KB = 128;              // bytes of K per stage: one scale block
 constexpr int LT_EPI = 8;               // epilogue warps: two per TMEM lane quadrant
-constexpr int LT_THREADS = 32 * (2 + LT_EPI);
-constexpr int LT_SS = 8;                // slots of the scale ring
+constexpr int LT_THREADS = 32 * (4 + LT_EPI);
+constexpr int LT_SC = 8;                // blocks of K of a scale slot
+constexpr int LT_SS = 2;                // slots of the scale ring
+constexpr int LT_REGS_CTRL = 56, LT_REGS_EPI = 224;   // 128 * 56 + 256 * 224 = 384 * 168, the launch's
 constexpr int LT_MAX_STAGES = 8;
 
 template <int BN>
@@ -169,7 +171,10 @@ struct LtShape {
     static constexpr int kSlots = BN >= 256 ? 2 : 4;                  // TMEM partial products
     static constexpr int kTmem = kSlots * BN;                          // columns
     static constexpr int kStage = (LT_BM + BN) * LT_KB;
-    static constexpr int kScale = (LT_BM + BN) * 4;                    // bytes of a scale slot
+    // a scale slot is [LT_SC][kLd] floats; 4 words over a multiple of 32, so that the copies of 4 rows by
+    // 8 blocks meet 32 banks
+    static constexpr int kLd = LT_BM + BN + 4;
+    static constexpr int kScale = LT_SC * kLd * 4;
     static constexpr int kCols = BN / 2;                               // columns of an epilogue warp
 };
 
@@ -211,18 +216,50 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void lt_tmem_ld16(uint32_t taddr, uint32_t* v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr));
+// CH columns of this lane's TMEM row.  The wait names the registers, so that nothing reads them before it.
+template <int CH>
+__device__ __forceinline__ void lt_tmem_ld(uint32_t taddr, uint32_t (&v)[CH]) {
+    if constexpr (CH == 32)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
+            "[%32];"
+            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+              "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+              "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]),
+              "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]),
+              "=r"(v[30]), "=r"(v[31])
+            : "r"(taddr));
+    else
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+              "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+            : "r"(taddr));
+}
+template <int CH>
+__device__ __forceinline__ void lt_tmem_wait(uint32_t (&v)[CH]) {
+    if constexpr (CH == 32)
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+                       "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]),
+                       "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]),
+                       "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]),
+                       "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
+    else
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+                       "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]),
+                       "+r"(v[14]), "+r"(v[15])::"memory");
 }
 
-// Persistent over the tiles, the row tiles of one weight tile first.  Warp 0: its lane 0 loads the
-// codes (TMA), its 32 lanes copy the stage's scales (their columns of the scale matrices); warp 1
-// issues the products; warps 2..9 sum and store.
+template <int N>
+__device__ __forceinline__ void lt_regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void lt_regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Persistent over the tiles, the row tiles of one weight tile first.  Warp 0 loads the codes (TMA), warp
+// 1 issues the products, warps 2 and 3 copy the scales, warps 4..11 sum and store.
 template <int BN>
 __global__ void __launch_bounds__(LT_THREADS, 1)
     linear_tile_kernel(const __grid_constant__ LinearMaps maps, LinearTileArgs a, DevCtx ctx) {
@@ -254,7 +291,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
             mbar_init(smem_u32(&pempty[p]), LT_EPI);
         }
         for (int s = 0; s < LT_SS; ++s) {
-            mbar_init(smem_u32(&sfull[s]), 32);
+            mbar_init(smem_u32(&sfull[s]), 64);
             mbar_init(smem_u32(&sempty[s]), LT_EPI);
         }
         mbar_init(smem_u32(drain), 1);
@@ -272,49 +309,66 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
 
     const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
     if (warp == 0) {
-        const uint64_t pol = l2_policy_evict_last();
-        int stage = 0, ss = 0;
-        uint32_t phase = 0, sph = 0;
-        bool ok = true;
-        for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const int m0 = (int)(t % a.m_tiles) * LT_BM, n0 = (int)(t / a.m_tiles) * BN;
-            for (int ks = 0; ks < l.kb; ++ks) {
-                int good = 1;
-                if (lane == 0) {
-                    good = mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, ctx, abort_flag) &&
-                                   mbar_wait(smem_u32(&sempty[ss]), sph ^ 1u, ctx, abort_flag)
-                               ? 1
-                               : 0;
-                    if (good) {
-                        const uint32_t fb = smem_u32(&full[stage]);
-                        mbar_arrive_expect_tx(fb, S::kStage);
-                        const uint32_t dst = smem_u32(smem + (size_t)stage * S::kStage);
-                        tma_load_2d(dst, &maps.x, fb, ks * LT_KB, m0, pol);
-                        tma_load_2d(dst + LT_BM * LT_KB, &maps.w, fb, ks * LT_KB, n0, pol);
+        lt_regs_dec<LT_REGS_CTRL>();
+        if (lane == 0) {
+            const uint64_t pol = l2_policy_evict_last();
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                const int m0 = (int)(t % a.m_tiles) * LT_BM, n0 = (int)(t / a.m_tiles) * BN;
+                for (int ks = 0; ks < l.kb; ++ks) {
+                    if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, ctx, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&full[stage]);
+                    mbar_arrive_expect_tx(fb, S::kStage);
+                    const uint32_t dst = smem_u32(smem + (size_t)stage * S::kStage);
+                    tma_load_2d(dst, &maps.x, fb, ks * LT_KB, m0, pol);
+                    tma_load_2d(dst + LT_BM * LT_KB, &maps.w, fb, ks * LT_KB, n0, pol);
+                    if (++stage == NS) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
                 }
-                if (!__shfl_sync(0xffffffffu, good, 0)) {
+            }
+            if (!ok || *abort_flag) {   // copies in flight land before the block may end
+                const uint64_t t0 = globaltimer();
+                while (globaltimer() - t0 < 200000ull) __nanosleep(1000);
+            }
+        }
+    } else if (warp == 2 || warp == 3) {
+        lt_regs_dec<LT_REGS_CTRL>();
+        // A copy takes 8 neighbouring blocks of 4 rows: the rows of the scale matrices are not aligned to
+        // more than 4 bytes, and 32 rows at a time would touch 32 lines.
+        const int kk = lane % LT_SC, r0 = (warp - 2) * 4 + lane / LT_SC;
+        int ss = 0;
+        uint32_t sph = 0;
+        bool ok = true;
+        for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const int64_t m0 = (t % a.m_tiles) * LT_BM;
+            const int n0 = (int)(t / a.m_tiles) * BN;
+            for (int ks = 0; ks < l.kb; ks += LT_SC) {
+                if (!mbar_wait_warp(smem_u32(&sempty[ss]), sph ^ 1u, ctx, abort_flag)) {
                     ok = false;
                     break;
                 }
-                const uint32_t sd = smem_u32(scales + ss * S::kScale);
-#pragma unroll
-                for (int i = 0; i < LT_BM / 32; ++i) {
-                    const int r = i * 32 + lane;
-                    const bool in = m0 + r < l.M;
-                    cp_async4(sd + r * 4, l.xs + (int64_t)(in ? m0 + r : 0) * l.kb + ks, in);
+                const bool in_k = ks + kk < l.kb;
+                const uint32_t sd = smem_u32(scales + ss * S::kScale) + (kk * S::kLd + r0) * 4;
+                const float* xs = l.xs + (m0 + r0) * l.kb + ks + kk;
+#pragma unroll 4
+                for (int r = 0; r < LT_BM; r += 8) {
+                    const bool in = in_k && m0 + r0 + r < l.M;
+                    cp_async4(sd + r * 4, in ? xs + r * l.kb : l.xs, in);
                 }
-#pragma unroll
-                for (int i = 0; i < BN / 32; ++i) {
-                    const int r = i * 32 + lane;
-                    const bool in = n0 + r < l.N;
-                    cp_async4(sd + (LT_BM + r) * 4, l.ws + (int64_t)(in ? n0 + r : 0) * l.kb + ks, in);
+                const float* ws = l.ws + (int64_t)(n0 + r0) * l.kb + ks + kk;
+#pragma unroll 4
+                for (int r = 0; r < BN; r += 8) {
+                    const bool in = in_k && n0 + r0 + r < l.N;
+                    cp_async4(sd + (LT_BM + r) * 4, in ? ws + r * l.kb : l.ws, in);
                 }
                 cp_async_arrive(smem_u32(&sfull[ss]));
-                if (++stage == NS) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
                 if (++ss == LT_SS) {
                     ss = 0;
                     sph ^= 1u;
@@ -322,11 +376,8 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if (!ok) {   // copies in flight land before the block may end
-            const uint64_t t0 = globaltimer();
-            while (globaltimer() - t0 < 200000ull) __nanosleep(1000);
-        }
     } else if (warp == 1) {
+        lt_regs_dec<LT_REGS_CTRL>();
         if (lane == 0) {
             const uint32_t idesc = make_idesc(0u, LT_BM, BN);
             int stage = 0, ps = 0;
@@ -365,9 +416,10 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
             }
         }
     } else {
+        lt_regs_inc<LT_REGS_EPI>();
         const int quad = warp & 3;                        // TMEM lanes 32 quad ..
-        const int c0 = (warp - 2) / 4 * S::kCols;         // columns c0 .. c0 + kCols
-        constexpr int CH = S::kCols < 32 ? S::kCols : 32;
+        const int c0 = (warp - 4) / 4 * S::kCols;         // columns c0 .. c0 + kCols
+        constexpr int CH = S::kCols < 32 ? S::kCols : 32, NC = S::kCols / CH;
         int ps = 0, ss = 0;
         uint32_t pph = 0, sph = 0;
         bool ok = true;
@@ -378,46 +430,51 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < S::kCols / 2; ++i) acc[i] = 0;
             for (int ks = 0; ks < l.kb; ++ks) {
-                if (!mbar_wait_warp(smem_u32(&sfull[ss]), sph, ctx, abort_flag) ||
+                const int kk = ks % LT_SC;
+                if ((kk == 0 && !mbar_wait_warp(smem_u32(&sfull[ss]), sph, ctx, abort_flag)) ||
                     !mbar_wait_warp(smem_u32(&pfull[ps]), pph, ctx, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const float* sc = reinterpret_cast<const float*>(scales + ss * S::kScale);
+                const float* sc = reinterpret_cast<const float*>(scales + ss * S::kScale) + kk * S::kLd;
                 const float sx = sc[quad * 32 + lane];
                 const uint64_t sx2 = f2_pack(sx, sx);
                 const float* sw = sc + LT_BM + c0;
                 const uint32_t ta = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(ps * BN + c0);
+                uint32_t v[2][CH];   // the next columns come while these are summed
+                lt_tmem_ld<CH>(ta, v[0]);
 #pragma unroll
-                for (int c = 0; c < S::kCols; c += CH) {
-                    uint32_t v[CH];
-                    lt_tmem_ld16(ta + c, v);
-                    if constexpr (CH == 32) lt_tmem_ld16(ta + c + 16, v + 16);
-                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                    if (c + CH == S::kCols) {   // the last read of the slot: free it before the sums
+                for (int c = 0; c < NC; ++c) {
+                    lt_tmem_wait<CH>(v[c % 2]);
+                    if (c + 1 < NC) lt_tmem_ld<CH>(ta + (c + 1) * CH, v[(c + 1) % 2]);
+                    else {   // the last read of the slot: free it before the sums
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_u32(&pempty[ps]));
                     }
 #pragma unroll
                     for (int j = 0; j < CH; j += 4) {
-                        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(sw + c + j);
-                        const uint64_t p0 = f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-                        const uint64_t p1 = f2_pack(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
-                        acc[(c + j) / 2] = f2_fma(f2_mul(p0, w.x), sx2, acc[(c + j) / 2]);
-                        acc[(c + j) / 2 + 1] = f2_fma(f2_mul(p1, w.y), sx2, acc[(c + j) / 2 + 1]);
+                        const int k = c * CH + j;
+                        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(sw + k);
+                        const uint32_t* p = v[c % 2] + j;
+                        const uint64_t p0 = f2_pack(__uint_as_float(p[0]), __uint_as_float(p[1]));
+                        const uint64_t p1 = f2_pack(__uint_as_float(p[2]), __uint_as_float(p[3]));
+                        acc[k / 2] = f2_fma(f2_mul(p0, w.x), sx2, acc[k / 2]);
+                        acc[k / 2 + 1] = f2_fma(f2_mul(p1, w.y), sx2, acc[k / 2 + 1]);
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sempty[ss]));
                 if (++ps == S::kSlots) {
                     ps = 0;
                     pph ^= 1u;
                 }
-                if (++ss == LT_SS) {
-                    ss = 0;
-                    sph ^= 1u;
+                if (kk == LT_SC - 1 || ks == l.kb - 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sempty[ss]));
+                    if (++ss == LT_SS) {
+                        ss = 0;
+                        sph ^= 1u;
+                    }
                 }
             }
             if (!ok) break;
