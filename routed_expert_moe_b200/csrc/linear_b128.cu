@@ -159,11 +159,10 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
 
 constexpr int LT_BM = 128;              // rows of x per tile (TMEM lanes)
 constexpr int LT_KB = 128;              // bytes of K per stage: one scale block
-constexpr int LT_EPI = 8;               // epilogue warps: two per TMEM lane quadrant
-constexpr int LT_THREADS = 32 * (4 + LT_EPI);
+constexpr int LT_MMA = 2;               // threads that issue products: the issue of one stage takes one thread
+                                        // about as long as the tensor core's work for a narrow tile
 constexpr int LT_SC = 8;                // blocks of K of a scale slot
 constexpr int LT_SS = 2;                // slots of the scale ring
-constexpr int LT_REGS_CTRL = 56, LT_REGS_EPI = 224;   // 128 * 56 + 256 * 224 = 384 * 168, the launch's
 constexpr int LT_MAX_STAGES = 8;
 
 template <int BN>
@@ -175,7 +174,11 @@ struct LtShape {
     // 8 blocks meet 32 banks
     static constexpr int kLd = LT_BM + BN + 4;
     static constexpr int kScale = LT_SC * kLd * 4;
-    static constexpr int kCols = BN / 2;                               // columns of an epilogue warp
+    static constexpr int kSets = BN >= 128 ? 4 : BN / 32;              // epilogue warps of a TMEM lane quadrant
+    static constexpr int kCols = BN / kSets;                           // columns of an epilogue warp
+    static constexpr int kThreads = 32 * (4 + 4 * kSets);
+    // 640 threads have 96 registers each at launch, too few for 64 sums: 128 * 56 + 512 * 104 <= 640 * 96
+    static constexpr bool kSplit = kSets == 4;
 };
 
 struct LinearTileArgs {
@@ -216,41 +219,38 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// CH columns of this lane's TMEM row.  The wait names the registers, so that nothing reads them before it.
-template <int CH>
-__device__ __forceinline__ void lt_tmem_ld(uint32_t taddr, uint32_t (&v)[CH]) {
-    if constexpr (CH == 32)
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
-            "[%32];"
-            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-              "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-              "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]),
-              "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]),
-              "=r"(v[30]), "=r"(v[31])
-            : "r"(taddr));
-    else
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-              "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-            : "r"(taddr));
+// 16 TMEM lanes by 32 columns: v[4 j + 2 i + e] is row lane / 4 + 8 i, column 8 j + 2 (lane % 4) + e.  So a
+// thread meets a quarter of the columns: with a row per thread each of them reads every column's scale,
+// and those reads (four cycles of shared memory for 16 bytes, however few addresses) took 1.2k cycles of
+// a stage of 128 x 256.  The wait names the registers, so that nothing reads them before it.
+__device__ __forceinline__ void lt_tmem_ld(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
 }
-template <int CH>
-__device__ __forceinline__ void lt_tmem_wait(uint32_t (&v)[CH]) {
-    if constexpr (CH == 32)
-        asm volatile("tcgen05.wait::ld.sync.aligned;"
-                     : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
-                       "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]),
-                       "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]),
-                       "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]),
-                       "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
-    else
-        asm volatile("tcgen05.wait::ld.sync.aligned;"
-                     : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
-                       "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]),
-                       "+r"(v[14]), "+r"(v[15])::"memory");
+__device__ __forceinline__ void lt_tmem_wait(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                   "+r"(v[15]));
+}
+
+// The four lanes of a quad hold one row's words of four 16-byte pieces, word l of each in lane l;
+// afterwards lane l holds piece l.
+__device__ __forceinline__ void lt_transpose(uint32_t (&p)[4], int l) {
+#pragma unroll
+    for (int d = 1; d <= 2; d *= 2) {
+        const bool hi = l & d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & d) continue;
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? p[i] : p[i + d], d);
+            if (hi) p[i] = got;
+            else p[i + d] = got;
+        }
+    }
 }
 
 template <int N>
@@ -258,10 +258,10 @@ __device__ __forceinline__ void lt_regs_inc() { asm volatile("setmaxnreg.inc.syn
 template <int N>
 __device__ __forceinline__ void lt_regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// Persistent over the tiles, the row tiles of one weight tile first.  Warp 0 loads the codes (TMA), warp
-// 1 issues the products, warps 2 and 3 copy the scales, warps 4..11 sum and store.
+// Persistent over the tiles, the row tiles of one weight tile first.  Warp 0 loads the codes (TMA), warps
+// 1 and 3 issue the products of even and odd stages, warp 2 copies the scales, the others sum and store.
 template <int BN>
-__global__ void __launch_bounds__(LT_THREADS, 1)
+__global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
     linear_tile_kernel(const __grid_constant__ LinearMaps maps, LinearTileArgs a, DevCtx ctx) {
     using S = LtShape<BN>;
     extern __shared__ uint8_t smem_raw[];
@@ -276,8 +276,8 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
     uint64_t* sfull = pempty + S::kSlots;
     uint64_t* sempty = sfull + LT_SS;
     uint64_t* drain = sempty + LT_SS;
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(drain + 1);
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1) + 1;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(drain + LT_MMA);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + LT_MMA) + 1;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const LinearArgs& l = a.l;
 
@@ -288,13 +288,13 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
         }
         for (int p = 0; p < S::kSlots; ++p) {
             mbar_init(smem_u32(&pfull[p]), 1);
-            mbar_init(smem_u32(&pempty[p]), LT_EPI);
+            mbar_init(smem_u32(&pempty[p]), 4 * S::kSets);
         }
         for (int s = 0; s < LT_SS; ++s) {
-            mbar_init(smem_u32(&sfull[s]), 64);
-            mbar_init(smem_u32(&sempty[s]), LT_EPI);
+            mbar_init(smem_u32(&sfull[s]), 32);
+            mbar_init(smem_u32(&sempty[s]), 4 * S::kSets);
         }
-        mbar_init(smem_u32(drain), 1);
+        for (int m = 0; m < LT_MMA; ++m) mbar_init(smem_u32(drain + m), 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&maps.x);
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
 
     const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
     if (warp == 0) {
-        lt_regs_dec<LT_REGS_CTRL>();
+        if constexpr (S::kSplit) lt_regs_dec<56>();
         if (lane == 0) {
             const uint64_t pol = l2_policy_evict_last();
             int stage = 0;
@@ -338,11 +338,11 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
                 while (globaltimer() - t0 < 200000ull) __nanosleep(1000);
             }
         }
-    } else if (warp == 2 || warp == 3) {
-        lt_regs_dec<LT_REGS_CTRL>();
+    } else if (warp == 2) {
+        if constexpr (S::kSplit) lt_regs_dec<56>();
         // A copy takes 8 neighbouring blocks of 4 rows: the rows of the scale matrices are not aligned to
         // more than 4 bytes, and 32 rows at a time would touch 32 lines.
-        const int kk = lane % LT_SC, r0 = (warp - 2) * 4 + lane / LT_SC;
+        const int kk = lane % LT_SC, r0 = lane / LT_SC;
         int ss = 0;
         uint32_t sph = 0;
         bool ok = true;
@@ -357,14 +357,14 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
                 const bool in_k = ks + kk < l.kb;
                 const uint32_t sd = smem_u32(scales + ss * S::kScale) + (kk * S::kLd + r0) * 4;
                 const float* xs = l.xs + (m0 + r0) * l.kb + ks + kk;
-#pragma unroll 4
-                for (int r = 0; r < LT_BM; r += 8) {
+#pragma unroll 8
+                for (int r = 0; r < LT_BM; r += 4) {
                     const bool in = in_k && m0 + r0 + r < l.M;
                     cp_async4(sd + r * 4, in ? xs + r * l.kb : l.xs, in);
                 }
                 const float* ws = l.ws + (int64_t)(n0 + r0) * l.kb + ks + kk;
-#pragma unroll 4
-                for (int r = 0; r < BN; r += 8) {
+#pragma unroll 8
+                for (int r = 0; r < BN; r += 4) {
                     const bool in = in_k && n0 + r0 + r < l.N;
                     cp_async4(sd + (LT_BM + r) * 4, in ? ws + r * l.kb : l.ws, in);
                 }
@@ -376,30 +376,32 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == 1) {
-        lt_regs_dec<LT_REGS_CTRL>();
+    } else if (warp < 4) {
+        if constexpr (S::kSplit) lt_regs_dec<56>();
         if (lane == 0) {
             const uint32_t idesc = make_idesc(0u, LT_BM, BN);
+            const uint32_t m = warp == 3;
             int stage = 0, ps = 0;
-            uint32_t phase = 0, pph = 0;
+            uint32_t phase = 0, pph = 0, n = 0;
             bool ok = true, issued = false;
             for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                for (int ks = 0; ks < l.kb; ++ks) {
-                    if (!mbar_wait(smem_u32(&full[stage]), phase, ctx, abort_flag) ||
-                        !mbar_wait(smem_u32(&pempty[ps]), pph ^ 1u, ctx, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t xa = smem_u32(smem + (size_t)stage * S::kStage);
-                    const uint32_t wa = xa + LT_BM * LT_KB;
+                for (int ks = 0; ks < l.kb; ++ks, ++n) {
+                    if (n % LT_MMA == m) {
+                        if (!mbar_wait(smem_u32(&full[stage]), phase, ctx, abort_flag) ||
+                            !mbar_wait(smem_u32(&pempty[ps]), pph ^ 1u, ctx, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t xa = smem_u32(smem + (size_t)stage * S::kStage);
+                        const uint64_t xd = sw128_desc(xa), wd = sw128_desc(xa + LT_BM * LT_KB);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)   // the block's sum: the slot is overwritten first
-                        mma_ss<true>(tmem_base + ps * BN, sw128_desc(xa + kk * 32), sw128_desc(wa + kk * 32), idesc,
-                                     kk != 0 ? 1u : 0u);
-                    issued = true;
-                    mma_commit(smem_u32(&empty[stage]));
-                    mma_commit(smem_u32(&pfull[ps]));
+                        for (int kk = 0; kk < 4; ++kk)   // the block's sum: the slot is overwritten first
+                            mma_ss<true>(tmem_base + ps * BN, xd + 2 * kk, wd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+                        issued = true;
+                        mma_commit(smem_u32(&empty[stage]));
+                        mma_commit(smem_u32(&pfull[ps]));
+                    }
                     if (++stage == NS) {
                         stage = 0;
                         phase ^= 1u;
@@ -410,25 +412,28 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
                     }
                 }
             }
-            if (!ok && issued) {
-                mma_commit(smem_u32(drain));
-                mbar_wait_drain(smem_u32(drain), 0, ctx.timeout_ns);
+            if ((!ok || *abort_flag) && issued) {
+                mma_commit(smem_u32(drain + m));
+                mbar_wait_drain(smem_u32(drain + m), 0, ctx.timeout_ns);
             }
         }
     } else {
-        lt_regs_inc<LT_REGS_EPI>();
+        if constexpr (S::kSplit) lt_regs_inc<104>();
         const int quad = warp & 3;                        // TMEM lanes 32 quad ..
         const int c0 = (warp - 4) / 4 * S::kCols;         // columns c0 .. c0 + kCols
-        constexpr int CH = S::kCols < 32 ? S::kCols : 32, NC = S::kCols / CH;
+        constexpr int NC = S::kCols / 32;
+        const int q = lane % 4, r0 = quad * 32 + lane / 4;
         int ps = 0, ss = 0;
         uint32_t pph = 0, sph = 0;
         bool ok = true;
         for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const int64_t m = (t % a.m_tiles) * LT_BM + quad * 32 + lane;
+            const int64_t m = (t % a.m_tiles) * LT_BM + r0;
             const int n0 = (int)(t / a.m_tiles) * BN + c0;
-            uint64_t acc[S::kCols / 2];
+            uint64_t acc[4][NC * 4];   // rows r0 + 8 i, columns 8 j + 2 q and the next
 #pragma unroll
-            for (int i = 0; i < S::kCols / 2; ++i) acc[i] = 0;
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < NC * 4; ++j) acc[i][j] = 0;
             for (int ks = 0; ks < l.kb; ++ks) {
                 const int kk = ks % LT_SC;
                 if ((kk == 0 && !mbar_wait_warp(smem_u32(&sfull[ss]), sph, ctx, abort_flag)) ||
@@ -438,30 +443,38 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
                 }
                 tc_fence_after();
                 const float* sc = reinterpret_cast<const float*>(scales + ss * S::kScale) + kk * S::kLd;
-                const float sx = sc[quad * 32 + lane];
-                const uint64_t sx2 = f2_pack(sx, sx);
-                const float* sw = sc + LT_BM + c0;
+                uint64_t sx[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sx[i] = f2_pack(sc[r0 + 8 * i], sc[r0 + 8 * i]);
+                const float* sw = sc + LT_BM + c0 + 2 * q;
                 const uint32_t ta = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(ps * BN + c0);
-                uint32_t v[2][CH];   // the next columns come while these are summed
-                lt_tmem_ld<CH>(ta, v[0]);
+                uint32_t v[2][16];   // the next values come while these are summed
+                lt_tmem_ld(ta, v[0]);
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    lt_tmem_wait<CH>(v[c % 2]);
-                    if (c + 1 < NC) lt_tmem_ld<CH>(ta + (c + 1) * CH, v[(c + 1) % 2]);
-                    else {   // the last read of the slot: free it before the sums
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&pempty[ps]));
-                    }
+                    uint64_t w[4];
 #pragma unroll
-                    for (int j = 0; j < CH; j += 4) {
-                        const int k = c * CH + j;
-                        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(sw + k);
-                        const uint32_t* p = v[c % 2] + j;
-                        const uint64_t p0 = f2_pack(__uint_as_float(p[0]), __uint_as_float(p[1]));
-                        const uint64_t p1 = f2_pack(__uint_as_float(p[2]), __uint_as_float(p[3]));
-                        acc[k / 2] = f2_fma(f2_mul(p0, w.x), sx2, acc[k / 2]);
-                        acc[k / 2 + 1] = f2_fma(f2_mul(p1, w.y), sx2, acc[k / 2 + 1]);
+                    for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint64_t*>(sw + c * 32 + j * 8);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {   // lanes 0 .. 15, 16 .. 31 of the quadrant
+                        uint32_t(&p)[16] = v[h];
+                        lt_tmem_wait(p);
+                        if (h == 0) lt_tmem_ld(ta + (16u << 16) + c * 32, v[1]);
+                        else if (c + 1 < NC) lt_tmem_ld(ta + (c + 1) * 32, v[0]);
+                        else {   // the last read of the slot: free it before the sums
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(&pempty[ps]));
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint64_t pp =
+                                    f2_pack(__uint_as_float(p[4 * j + 2 * i]), __uint_as_float(p[4 * j + 2 * i + 1]));
+                                uint64_t& s = acc[2 * h + i][4 * c + j];
+                                s = f2_fma(f2_mul(pp, w[j]), sx[2 * h + i], s);
+                            }
                     }
                 }
                 if (++ps == S::kSlots) {
@@ -478,22 +491,23 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
                 }
             }
             if (!ok) break;
-            if (m < l.M) {
-                uint16_t* o = l.out + m * l.N + n0;
 #pragma unroll
-                for (int c = 0; c < S::kCols; c += 8) {
-                    if (n0 + c >= l.N) break;   // N is a multiple of 16
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
                     uint32_t w[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         float lo, hi;
-                        f2_unpack(acc[c / 2 + j], lo, hi);
+                        f2_unpack(acc[i][4 * c + j], lo, hi);
                         const __nv_bfloat162 b = __floats2bfloat162_rn(lin_act(lo, l.relu2), lin_act(hi, l.relu2));
                         w[j] = *reinterpret_cast<const uint32_t*>(&b);
                     }
-                    *reinterpret_cast<uint4*>(o + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                    lt_transpose(w, q);   // now 8 columns in a row, a quad 64 bytes
+                    const int n = n0 + c * 32 + q * 8;
+                    if (m + 8 * i < l.M && n < l.N)   // N is a multiple of 16
+                        *reinterpret_cast<uint4*>(l.out + (m + 8 * i) * l.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-            }
         }
     }
 
@@ -557,14 +571,14 @@ static cudaError_t launch_linear_tiles(const LinearArgs& l, int num_sms, const D
     a.l = l;
     a.m_tiles = (int)((l.M + LT_BM - 1) / LT_BM);
     a.n_tiles = (l.N + BN - 1) / BN;
-    const size_t fixed = 1024 + LT_SS * S::kScale + (2 * LT_MAX_STAGES + 2 * S::kSlots + 2 * LT_SS + 1) * 8 + 16;
+    const size_t fixed = 1024 + LT_SS * S::kScale + (2 * LT_MAX_STAGES + 2 * S::kSlots + 2 * LT_SS + LT_MMA) * 8 + 16;
     a.n_stages = (int)std::min<size_t>(LT_MAX_STAGES, (FW_SMEM - fixed) / S::kStage);
     const size_t smem = (size_t)a.n_stages * S::kStage + fixed;
     auto k = linear_tile_kernel<BN>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t grid = std::min<int64_t>((int64_t)a.m_tiles * a.n_tiles, num_sms);
-    return launch_k(k, dim3((unsigned)grid), dim3(LT_THREADS), smem, stream, maps, a, ctx);
+    return launch_k(k, dim3((unsigned)grid), dim3(S::kThreads), smem, stream, maps, a, ctx);
 }
 
 static cudaError_t launch_linear(const LinearArgs& l, int num_sms, const DevCtx& ctx, cudaStream_t stream) {
