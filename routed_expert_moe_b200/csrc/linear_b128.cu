@@ -167,18 +167,16 @@ constexpr int LT_MAX_STAGES = 8;
 
 template <int BN>
 struct LtShape {
-    static constexpr int kSlots = BN >= 256 ? 2 : 4;                  // TMEM partial products
+    static constexpr int kSlots = 4;                  // TMEM partial products
     static constexpr int kTmem = kSlots * BN;                          // columns
     static constexpr int kStage = (LT_BM + BN) * LT_KB;
     // a scale slot is [LT_SC][kLd] floats; 4 words over a multiple of 32, so that the copies of 4 rows by
     // 8 blocks meet 32 banks
     static constexpr int kLd = LT_BM + BN + 4;
     static constexpr int kScale = LT_SC * kLd * 4;
-    static constexpr int kSets = BN >= 128 ? 4 : BN / 32;              // epilogue warps of a TMEM lane quadrant
+    static constexpr int kSets = BN >= 64 ? 2 : 1;                    // epilogue warps of a TMEM lane quadrant
     static constexpr int kCols = BN / kSets;                           // columns of an epilogue warp
     static constexpr int kThreads = 32 * (4 + 4 * kSets);
-    // 640 threads have 96 registers each at launch, too few for 64 sums: 128 * 56 + 512 * 104 <= 640 * 96
-    static constexpr bool kSplit = kSets == 4;
 };
 
 struct LinearTileArgs {
@@ -208,15 +206,6 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
-}
-
-// 4-byte asynchronous copy to shared memory; zero when !valid (the address must be readable anyway).
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
-    const int n = valid ? 4 : 0;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // 16 TMEM lanes by 32 columns: v[4 j + 2 i + e] is row lane / 4 + 8 i, column 8 j + 2 (lane % 4) + e.  So a
@@ -253,10 +242,27 @@ __device__ __forceinline__ void lt_transpose(uint32_t (&p)[4], int l) {
     }
 }
 
-template <int N>
-__device__ __forceinline__ void lt_regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void lt_regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// Every lane looks for itself, and only a wait that is not over takes the slow way: one lane's look and a
+// shuffle of what it saw cost each stage of a warp more than its sums.
+__device__ __forceinline__ bool lt_wait(uint32_t bar, uint32_t parity, const DevCtx& ctx, volatile int* abort) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return mbar_wait_warp(bar, parity, ctx, abort);
+}
+
+// A warp's wait for something thousands of cycles away.
+__device__ __forceinline__ bool lt_wait_long(uint32_t bar, uint32_t parity, const DevCtx& ctx, volatile int* abort) {
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort) return false;
+        if (globaltimer() - t0 > ctx.timeout_ns) {
+            record_error(ctx.err, MOE_ETIMEOUT);
+            *abort = 1;
+            return false;
+        }
+        __nanosleep(500);
+    }
+    return true;
+}
 
 // Persistent over the tiles, the row tiles of one weight tile first.  Warp 0 loads the codes (TMA), warps
 // 1 and 3 issue the products of even and odd stages, warp 2 copies the scales, the others sum and store.
@@ -291,7 +297,7 @@ __global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
             mbar_init(smem_u32(&pempty[p]), 4 * S::kSets);
         }
         for (int s = 0; s < LT_SS; ++s) {
-            mbar_init(smem_u32(&sfull[s]), 32);
+            mbar_init(smem_u32(&sfull[s]), 1);
             mbar_init(smem_u32(&sempty[s]), 4 * S::kSets);
         }
         for (int m = 0; m < LT_MMA; ++m) mbar_init(smem_u32(drain + m), 1);
@@ -309,7 +315,6 @@ __global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
 
     const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
     if (warp == 0) {
-        if constexpr (S::kSplit) lt_regs_dec<56>();
         if (lane == 0) {
             const uint64_t pol = l2_policy_evict_last();
             int stage = 0;
@@ -339,9 +344,10 @@ __global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
             }
         }
     } else if (warp == 2) {
-        if constexpr (S::kSplit) lt_regs_dec<56>();
-        // A copy takes 8 neighbouring blocks of 4 rows: the rows of the scale matrices are not aligned to
-        // more than 4 bytes, and 32 rows at a time would touch 32 lines.
+        // A read takes 8 neighbouring blocks of 4 rows: the rows of the scale matrices are not aligned to
+        // more than 4 bytes, and 32 rows at a time would touch 32 lines.  Through registers: as 4-byte
+        // asynchronous copies they took 180 cycles each, 17k for the 8 blocks of a tile of 128 x 256, and
+        // held up the shared memory reads of the sums on the same scheduler.
         const int kk = lane % LT_SC, r0 = lane / LT_SC;
         int ss = 0;
         uint32_t sph = 0;
@@ -350,34 +356,34 @@ __global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
             const int64_t m0 = (t % a.m_tiles) * LT_BM;
             const int n0 = (int)(t / a.m_tiles) * BN;
             for (int ks = 0; ks < l.kb; ks += LT_SC) {
-                if (!mbar_wait_warp(smem_u32(&sempty[ss]), sph ^ 1u, ctx, abort_flag)) {
+                if (!__all_sync(0xffffffffu, lt_wait_long(smem_u32(&sempty[ss]), sph ^ 1u, ctx, abort_flag))) {
                     ok = false;
                     break;
                 }
                 const bool in_k = ks + kk < l.kb;
-                const uint32_t sd = smem_u32(scales + ss * S::kScale) + (kk * S::kLd + r0) * 4;
+                float* sd = reinterpret_cast<float*>(scales + ss * S::kScale) + kk * S::kLd + r0;
                 const float* xs = l.xs + (m0 + r0) * l.kb + ks + kk;
-#pragma unroll 8
-                for (int r = 0; r < LT_BM; r += 4) {
-                    const bool in = in_k && m0 + r0 + r < l.M;
-                    cp_async4(sd + r * 4, in ? xs + r * l.kb : l.xs, in);
-                }
                 const float* ws = l.ws + (int64_t)(n0 + r0) * l.kb + ks + kk;
-#pragma unroll 8
-                for (int r = 0; r < BN; r += 4) {
-                    const bool in = in_k && n0 + r0 + r < l.N;
-                    cp_async4(sd + (LT_BM + r) * 4, in ? ws + r * l.kb : l.ws, in);
-                }
-                cp_async_arrive(smem_u32(&sfull[ss]));
+                const int step = 4 * l.kb, mx = in_k ? (int)min((int64_t)LT_BM, l.M - m0) : 0;
+                const int mw = in_k ? min(BN, l.N - n0) : 0;
+                float vx[LT_BM / 4], vw[BN / 4];   // all in flight
+#pragma unroll
+                for (int i = 0; i < LT_BM / 4; ++i) vx[i] = r0 + 4 * i < mx ? __ldg(xs + i * step) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < BN / 4; ++i) vw[i] = r0 + 4 * i < mw ? __ldg(ws + i * step) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < LT_BM / 4; ++i) sd[4 * i] = vx[i];
+#pragma unroll
+                for (int i = 0; i < BN / 4; ++i) sd[LT_BM + 4 * i] = vw[i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sfull[ss]));
                 if (++ss == LT_SS) {
                     ss = 0;
                     sph ^= 1u;
                 }
             }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp < 4) {
-        if constexpr (S::kSplit) lt_regs_dec<56>();
         if (lane == 0) {
             const uint32_t idesc = make_idesc(0u, LT_BM, BN);
             const uint32_t m = warp == 3;
@@ -418,14 +424,15 @@ __global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
             }
         }
     } else {
-        if constexpr (S::kSplit) lt_regs_inc<104>();
         const int quad = warp & 3;                        // TMEM lanes 32 quad ..
         const int c0 = (warp - 4) / 4 * S::kCols;         // columns c0 .. c0 + kCols
         constexpr int NC = S::kCols / 32;
         const int q = lane % 4, r0 = quad * 32 + lane / 4;
+        const uint32_t tq = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)c0;
         int ps = 0, ss = 0;
         uint32_t pph = 0, sph = 0;
         bool ok = true;
+        uint32_t v[2][16];   // the next values come while these are summed
         for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
             const int64_t m = (t % a.m_tiles) * LT_BM + r0;
             const int n0 = (int)(t / a.m_tiles) * BN + c0;
@@ -434,22 +441,17 @@ __global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < NC * 4; ++j) acc[i][j] = 0;
-            for (int ks = 0; ks < l.kb; ++ks) {
-                const int kk = ks % LT_SC;
-                if ((kk == 0 && !mbar_wait_warp(smem_u32(&sfull[ss]), sph, ctx, abort_flag)) ||
-                    !mbar_wait_warp(smem_u32(&pfull[ps]), pph, ctx, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+            ok = lt_wait(smem_u32(&sfull[ss]), sph, ctx, abort_flag) && lt_wait(smem_u32(&pfull[ps]), pph, ctx, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            lt_tmem_ld(tq + ps * BN, v[0]);
+            for (int ks = 0, kk = 0; ks < l.kb; ++ks) {
                 const float* sc = reinterpret_cast<const float*>(scales + ss * S::kScale) + kk * S::kLd;
                 uint64_t sx[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sx[i] = f2_pack(sc[r0 + 8 * i], sc[r0 + 8 * i]);
                 const float* sw = sc + LT_BM + c0 + 2 * q;
-                const uint32_t ta = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(ps * BN + c0);
-                uint32_t v[2][16];   // the next values come while these are summed
-                lt_tmem_ld(ta, v[0]);
+                const bool chunk_end = ++kk == LT_SC;
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
                     uint64_t w[4];
@@ -459,12 +461,22 @@ __global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
                     for (int h = 0; h < 2; ++h) {   // lanes 0 .. 15, 16 .. 31 of the quadrant
                         uint32_t(&p)[16] = v[h];
                         lt_tmem_wait(p);
-                        if (h == 0) lt_tmem_ld(ta + (16u << 16) + c * 32, v[1]);
-                        else if (c + 1 < NC) lt_tmem_ld(ta + (c + 1) * 32, v[0]);
-                        else {   // the last read of the slot: free it before the sums
+                        if (h == 0) lt_tmem_ld(tq + ps * BN + (16u << 16) + c * 32, v[1]);
+                        else if (c + 1 < NC) lt_tmem_ld(tq + ps * BN + (c + 1) * 32, v[0]);
+                        else {   // the last read of the slot: free it, go on to the next
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(smem_u32(&pempty[ps]));
+                            if (++ps == S::kSlots) {
+                                ps = 0;
+                                pph ^= 1u;
+                            }
+                            if (ks + 1 < l.kb) {
+                                ok = lt_wait(smem_u32(&pfull[ps]), pph, ctx, abort_flag);
+                                if (!ok) break;
+                                tc_fence_after();
+                                lt_tmem_ld(tq + ps * BN, v[0]);
+                            }
                         }
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
@@ -477,16 +489,18 @@ __global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
                             }
                     }
                 }
-                if (++ps == S::kSlots) {
-                    ps = 0;
-                    pph ^= 1u;
-                }
-                if (kk == LT_SC - 1 || ks == l.kb - 1) {
+                if (!ok) break;
+                if (chunk_end || ks == l.kb - 1) {
+                    kk = 0;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sempty[ss]));
                     if (++ss == LT_SS) {
                         ss = 0;
                         sph ^= 1u;
+                    }
+                    if (ks + 1 < l.kb) {
+                        ok = lt_wait(smem_u32(&sfull[ss]), sph, ctx, abort_flag);
+                        if (!ok) break;
                     }
                 }
             }
@@ -593,7 +607,6 @@ static cudaError_t launch_linear(const LinearArgs& l, int num_sms, const DevCtx&
     // the widest tile that still gives every SM one
     const int64_t mt = (l.M + LT_BM - 1) / LT_BM;
     auto fills = [&](int bn) { return mt * ((l.N + bn - 1) / bn) >= num_sms; };
-    if (fills(256)) return launch_linear_tiles<256>(l, num_sms, ctx, stream);
     if (fills(128)) return launch_linear_tiles<128>(l, num_sms, ctx, stream);
     if (fills(64)) return launch_linear_tiles<64>(l, num_sms, ctx, stream);
     return launch_linear_tiles<32>(l, num_sms, ctx, stream);
