@@ -276,33 +276,26 @@ def rmsnorm(x, u, eps=1e-5, stream=None):
     _check(_lib.moe_rmsnorm(T, H, float(eps), _ptr(x), _ptr(u), _stream(stream)), "moe_rmsnorm")
 
 
-def _arg(t, where, dtype, *shape):
-    """Pointer of a dense tensor of this type and shape on the current device (None passes through)."""
-    import torch
+def _arg(t, where, dtype, shape, device):
+    """Pointer of a dense tensor of this type and shape on this device (None passes through)."""
     if t is None:
         return None
-    if (t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous()
-            or t.get_device() != torch.cuda.current_device()):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
         raise MoeError(MOE_EINVAL, f"{where}: needs a contiguous {dtype} tensor of shape {shape} on the current "
                                    f"CUDA device, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
-
-
-def _codes(codes, scales, where, rows, K):
-    import torch
-    kp = b128_kp(K)
-    return (_arg(codes, where, torch.uint8, rows, kp), _arg(scales, where, torch.float32, rows, kp // 128))
 
 
 def prenorm(x, gain=None, u=None, codes=None, scales=None, eps=1e-5, stream=None):
     """The norm before a block: x [T, H] bf16 / rms * gain into u [T, H] (bf16) and / or FP8_B128 codes
     [T, b128_kp(H)] with scales [T, b128_kp(H) / 128]."""
     import torch
-    bf, w = torch.bfloat16, "moe_prenorm"
-    T, H = x.shape
-    c, s = _codes(codes, scales, w, T, H)
-    _check(_lib.moe_prenorm(T, H, eps, _arg(x, w, bf, T, H), _arg(gain, w, bf, H), _arg(u, w, bf, T, H), c, s,
-                            _stream(stream)), w)
+    bf, w, dev = torch.bfloat16, "moe_prenorm", torch.cuda.current_device()
+    T, H = th = x.shape
+    kp = (H + 127) // 128 * 128
+    _check(_lib.moe_prenorm(T, H, eps, _arg(x, w, bf, th, dev), _arg(gain, w, bf, (H,), dev), _arg(u, w, bf, th, dev),
+                            _arg(codes, w, torch.uint8, (T, kp), dev),
+                            _arg(scales, w, torch.float32, (T, kp // 128), dev), _stream(stream)), w)
 
 
 def postnorm(y, gain, x, x_out, gate=None, alpha=1.0, eps=1e-5, next_gain=None, u=None, codes=None, scales=None,
@@ -310,14 +303,15 @@ def postnorm(y, gain, x, x_out, gate=None, alpha=1.0, eps=1e-5, next_gain=None, 
     """x_out = x + alpha * gate * (y / rms(y) * gain); then prenorm of that sum with next_gain into u and / or
     codes, scales (none of them: x_out only).  gate: [H] or [T, H] or None."""
     import torch
-    bf, w = torch.bfloat16, "moe_postnorm"
-    T, H = x.shape
-    c, s = _codes(codes, scales, w, T, H)
+    bf, w, dev = torch.bfloat16, "moe_postnorm", torch.cuda.current_device()
+    T, H = th = x.shape
+    kp = (H + 127) // 128 * 128
     per_token = gate is not None and gate.dim() == 2
-    g = _arg(gate, w, bf, T, H) if per_token else _arg(gate, w, bf, H)
-    _check(_lib.moe_postnorm(T, H, eps, alpha, _arg(y, w, bf, T, H), _arg(gain, w, bf, H), g, H if per_token else 0,
-                             _arg(x, w, bf, T, H), _arg(x_out, w, bf, T, H), _arg(next_gain, w, bf, H),
-                             _arg(u, w, bf, T, H), c, s, _stream(stream)), w)
+    _check(_lib.moe_postnorm(T, H, eps, alpha, _arg(y, w, bf, th, dev), _arg(gain, w, bf, (H,), dev),
+                             _arg(gate, w, bf, th if per_token else (H,), dev), H if per_token else 0,
+                             _arg(x, w, bf, th, dev), _arg(x_out, w, bf, th, dev), _arg(next_gain, w, bf, (H,), dev),
+                             _arg(u, w, bf, th, dev), _arg(codes, w, torch.uint8, (T, kp), dev),
+                             _arg(scales, w, torch.float32, (T, kp // 128), dev), _stream(stream)), w)
 
 
 MOE_ACT_NONE, MOE_ACT_RELU2 = 0, 1
@@ -328,15 +322,15 @@ def linear_fp8_b128(x_codes, x_scales, w_codes, w_scales, out, act=None, stream=
     """out [M, N] (bf16) = act(x w^T) of FP8_B128 operands: codes [rows, Kp] (uint8, Kp a multiple of 128), scales
     [rows, Kp / 128] (fp32); act: None or "relu2"."""
     import torch
-    w = "moe_linear_fp8_b128"
+    w, dev, u8, f32 = "moe_linear_fp8_b128", torch.cuda.current_device(), torch.uint8, torch.float32
     M, Kp = x_codes.shape
     N = w_codes.shape[0]
     if act not in _ACTS or Kp % 128:
         raise MoeError(MOE_EINVAL, f"{w}: act {act!r}, code rows of {Kp} bytes")
-    xc, xs = _codes(x_codes, x_scales, w, M, Kp)
-    wc, ws = _codes(w_codes, w_scales, w, N, Kp)
-    _check(_lib.moe_linear_fp8_b128(M, N, Kp, xc, xs, wc, ws, _ACTS[act], _arg(out, w, torch.bfloat16, M, N),
-                                    _stream(stream)), w)
+    _check(_lib.moe_linear_fp8_b128(M, N, Kp, _arg(x_codes, w, u8, (M, Kp), dev),
+                                    _arg(x_scales, w, f32, (M, Kp // 128), dev),
+                                    _arg(w_codes, w, u8, (N, Kp), dev), _arg(w_scales, w, f32, (N, Kp // 128), dev),
+                                    _ACTS[act], _arg(out, w, torch.bfloat16, (M, N), dev), _stream(stream)), w)
 
 
 def check_device_error(stream=None):

@@ -73,60 +73,70 @@ __device__ __forceinline__ float nm_block_sum(float v, float* red, int n_warps) 
     return s;
 }
 
-// One block per row at a time (grid-stride); thread i holds the row's 16-byte vectors
-// i + j * blockDim.x, j < VPT.
-template <int VPT, bool POST, bool CODES>
-__global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
+// A block per row at a time (grid-stride); thread i of its n holds the row's 16-byte vectors i + j * n,
+// j < VPT.
+template <int VPT, int MAXT, bool POST, bool CODES>
+__global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 768 / MAXT) norm_kernel(NormArgs a) {
     pdl_enter();
     __shared__ float red[2][2][32];   // [row parity][sum][warp]
     const int nv = a.H / 8;
     const int kb = (a.H + 127) / 128;
-    const int n_warps = blockDim.x / 32;
+    const int i0 = threadIdx.x, n = blockDim.x;
     int par = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, par ^= 1) {
-        uint4 xq[VPT], yq[VPT];
+        uint4 xq[VPT];
         const uint4* xr = reinterpret_cast<const uint4*>(a.x + t * a.H);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
+            const int v = i0 + j * n;
             xq[j] = v < nv ? xr[v] : make_uint4(0, 0, 0, 0);
         }
         float f[VPT][8];
         if constexpr (POST) {
             const uint4* yr = reinterpret_cast<const uint4*>(a.y + t * a.H);
+            uint4 yq[VPT];
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = i0 + j * n;
+                yq[j] = v < nv ? yr[v] : make_uint4(0, 0, 0, 0);
+            }
             float ss = 0.0f;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int v = threadIdx.x + j * blockDim.x;
-                yq[j] = v < nv ? yr[v] : make_uint4(0, 0, 0, 0);
-                nm_unpack(yq[j], f[j]);
+                float y[8];
+                nm_unpack(yq[j], y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = __fmaf_rn(f[j][i], f[j][i], ss);
+                for (int i = 0; i < 8; ++i) ss = __fmaf_rn(y[i], y[i], ss);
             }
-            ss = nm_block_sum(ss, red[par][0], n_warps);
+            ss = nm_block_sum(ss, red[par][0], n / 32);
             const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)a.H), a.eps));
             uint4* xo = reinterpret_cast<uint4*>(a.x_out + t * a.H);
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int v = threadIdx.x + j * blockDim.x;
-                if (v >= nv) break;
+                const int v = i0 + j * n;
                 float p[8], xx[8];
+                nm_unpack(yq[j], f[j]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[j][i] *= r;
-                if (a.gain_post) {
-                    nm_unpack(reinterpret_cast<const uint4*>(a.gain_post)[v], p);
+                if (v < nv) {
+                    if (a.gain_post) {
+                        nm_unpack(reinterpret_cast<const uint4*>(a.gain_post)[v], p);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[j][i] *= p[i];
+                        for (int i = 0; i < 8; ++i) f[j][i] *= p[i];
+                    }
+                    if (a.gate) {
+                        nm_unpack(reinterpret_cast<const uint4*>(a.gate + t * a.gate_ld)[v], p);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[j][i] *= p[i];
+                    }
+                    nm_unpack(xq[j], xx);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[j][i] = __fmaf_rn(a.alpha, f[j][i], xx[i]);
+                    xo[v] = nm_pack(f[j]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[j][i] = 0.0f;   // also where the row's r is not finite
                 }
-                if (a.gate) {
-                    nm_unpack(reinterpret_cast<const uint4*>(a.gate + t * a.gate_ld)[v], p);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[j][i] *= p[i];
-                }
-                nm_unpack(xq[j], xx);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[j][i] = __fmaf_rn(a.alpha, f[j][i], xx[i]);
-                xo[v] = nm_pack(f[j]);
             }
         } else {
 #pragma unroll
@@ -138,13 +148,13 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss = __fmaf_rn(f[j][i], f[j][i], ss);
-        ss = nm_block_sum(ss, red[par][1], n_warps);
+        ss = nm_block_sum(ss, red[par][1], n / 32);
         const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)a.H), a.eps));
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
+            const int v = i0 + j * n;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[j][i] *= r;
+            for (int i = 0; i < 8; ++i) f[j][i] = v < nv ? f[j][i] * r : 0.0f;
             if (a.gain_pre && v < nv) {
                 float p[8];
                 nm_unpack(reinterpret_cast<const uint4*>(a.gain_pre)[v], p);
@@ -159,12 +169,18 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
                 for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[j][i]));
 #pragma unroll
                 for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                const float s = m > 0.0f ? __fdiv_rn(m, 448.0f) : 1.0f;
+                // Not below the smallest normal number, so that 1 / s is finite.  A product with it is
+                // within 2^-23 of the quotient, next to half a step of the codes, 2^-4; a quotient per
+                // value took longer than the bytes.
+                const float s = m > 0.0f ? fmaxf(__fdiv_rn(m, 448.0f), 0x1p-126f) : 1.0f;
+                const float is = __frcp_rn(s);
                 if (v < kb * 16) {
                     uint32_t c[2] = {0, 0};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        c[i / 4] |= (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(f[j][i], s), __NV_SATFINITE, __NV_E4M3)
+                    for (int i = 0; i < 8; i += 2)
+                        c[i / 4] |= (uint32_t)__nv_cvt_float2_to_fp8x2(
+                                        make_float2(__fmul_rn(f[j][i], is), __fmul_rn(f[j][i + 1], is)),
+                                        __NV_SATFINITE, __NV_E4M3)
                                     << (8 * (i % 4));
                     *reinterpret_cast<uint2*>(a.codes + (t * kb * 16 + v) * 8) = make_uint2(c[0], c[1]);
                     if (v % 16 == 0) a.scales[t * kb + v / 16] = s;
@@ -176,30 +192,39 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
 
 // ----------------------------------------------------------------------------- host
 
-template <int VPT>
+template <int VPT, int MAXT>
 static cudaError_t launch_vpt(const NormArgs& a, int threads, int num_sms, cudaStream_t stream) {
     const bool post = a.y != nullptr, codes = a.codes != nullptr;
-    void (*k)(NormArgs) = post ? (codes ? norm_kernel<VPT, true, true> : norm_kernel<VPT, true, false>)
-                               : (codes ? norm_kernel<VPT, false, true> : norm_kernel<VPT, false, false>);
-    int per_sm = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, 0);
-    if (e != cudaSuccess) return e;
-    const int64_t grid = std::min(a.T, (int64_t)num_sms * std::max(per_sm, 1));
+    void (*k)(NormArgs) = post ? (codes ? norm_kernel<VPT, MAXT, true, true> : norm_kernel<VPT, MAXT, true, false>)
+                               : (codes ? norm_kernel<VPT, MAXT, false, true> : norm_kernel<VPT, MAXT, false, false>);
+    // a row for each block, up to a grid that only takes time to launch: with as many blocks as fit, each
+    // with several rows, a row's loads wait for the stores of the one before (pre, 16384 rows: 32 -> 40 us)
+    const int64_t grid = std::min<int64_t>(a.T, 1024 * num_sms);
     return launch_k(k, dim3((unsigned)grid), dim3((unsigned)threads), 0, stream, a);
 }
 
 static cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t stream) {
     // vectors of a row, a whole number of 128-value blocks
     const int nv = (a.H + 127) / 128 * 16;
-    int vpt = 1;
-    while ((nv + vpt - 1) / vpt > 1024) vpt *= 2;
-    const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
-    switch (vpt) {
-        case 1: return launch_vpt<1>(a, threads, num_sms, stream);
-        case 2: return launch_vpt<2>(a, threads, num_sms, stream);
-        case 4: return launch_vpt<4>(a, threads, num_sms, stream);
-        default: return launch_vpt<8>(a, threads, num_sms, stream);
+    // With three rows or more for every SM, several small blocks of an SM work at once, and a thread has
+    // three or four vectors of each input under way; with fewer, a vector per thread has the least latency.
+    // Device times, H = 2688 (one vector against three), prenorm to u and postnorm to x', u:
+    //   T = 296    2.7 against 3.1 us,   4.3 against  5.7
+    //   T = 577    4.3 against 3.5,      7.6 against  6.6
+    //   T = 16384   58 against  32,      153 against   93       (a warp per row: 35, 117)
+    if (a.T >= 3 * num_sms) {
+        const int w = (nv + 127) / 128;
+        if (w <= 2) return launch_vpt<2, 128>(a, 128, num_sms, stream);
+        if (w <= 3) return launch_vpt<3, 128>(a, 128, num_sms, stream);
+        if (w <= 4) return launch_vpt<4, 128>(a, 128, num_sms, stream);
+        if (w <= 8) return launch_vpt<4, 256>(a, 256, num_sms, stream);
+        if (w <= 16) return launch_vpt<4, 512>(a, 512, num_sms, stream);
     }
+    auto threads = [&](int vpt) { return ((nv + vpt - 1) / vpt + 31) / 32 * 32; };
+    if (nv <= 1024) return launch_vpt<1, 1024>(a, threads(1), num_sms, stream);
+    if (nv <= 2048) return launch_vpt<2, 1024>(a, threads(2), num_sms, stream);
+    if (nv <= 4096) return launch_vpt<4, 1024>(a, threads(4), num_sms, stream);
+    return launch_vpt<8, 1024>(a, threads(8), num_sms, stream);
 }
 
 }  // namespace moe
