@@ -22,9 +22,19 @@
 // Units are claimed in list order, so those that a unit waits for belong to CTAs that run; no CTA
 // needs another to be resident, and every wait is bounded.
 //
-// Bound: HBM bytes of the touched experts' weights.  128-row units leave SMs without work at one or two
-// tokens (87 up units at one token of the full sizes), which costs little: a load-only loop of 60 MB
-// takes 16.4 us on 87 SMs and on 148.
+// Bound: HBM bytes of the touched experts' weights, at one to three tokens the fixed steps around them:
+// two launches, the choice of experts (3 us), a first and a last unit with nothing beside them.  128-row
+// units leave SMs without work at one or two tokens (87 up units at one token of the full sizes), which
+// costs little: a load-only loop of 60 MB takes 16.4 us on 87 SMs and on 148.  Units of 64 rows while
+// there are few were slower (bf16, 3 tokens: 92 against 72 us): a stage of half the weights takes the
+// same products.
+//
+// H = 2688, E = 128, K = 6, F = 1856, us, against moe_forward, and what the touched weights take at the
+// rate of a copy:
+//   tokens       1                   4                   8                     16
+//   bf16    40 / 53 / 19        88 / 95 / 69       137 / 143 / 129       218 / 215 / 214
+//   E4M3    35 / 41 /  9        51 / 65 / 35        82 /  90 /  64       126 / 127 / 107
+//   B128    37 / 45 / 10        55 / 71 / 36        85 /  96 /  68       130 / 134 / 112
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -172,7 +182,7 @@ __global__ void __launch_bounds__(FEW_RT) few_router_kernel(FewRouterArgs a, Dev
 
 // ----------------------------------------------------------------------------- layer
 
-constexpr int FL_THREADS = 384;     // weights, two of products, four of the epilogue, columns; all route
+constexpr int FL_THREADS = 384;     // weights, two of products, columns, two sets of four of the epilogue; all route
 constexpr int FL_MMA = 2;           // warps that issue products: of the even and of the odd stages
 constexpr int FL_BM = 128;          // weight rows per unit
 constexpr int FL_KB = 128;          // bytes of K per stage (E4M3: one scale block)

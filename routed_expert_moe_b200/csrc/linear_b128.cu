@@ -8,19 +8,23 @@
 // operand, fp32 sums.  Two kernels by the number of rows M:
 //
 //  - M <= 16: a weight stream.  Every CTA owns an equal share of the N weight
-//    rows over the whole of K (few.cuh: bulk-copy ring, warp-level products,
-//    eight warps split K and add their sums once).  Bound: HBM bytes.
+//    rows over the whole of K (weight_stream.cuh); eight warps split K and add
+//    their sums once.  Bound: HBM bytes and the launch.
 //  - above: tcgen05 tiles of 128 rows of x by BN rows of w.  A 128-byte K
 //    stage is one scale block, so its product goes to a TMEM slot of its own
-//    and eight epilogue warps, which hold the tile's fp32 sums in registers,
-//    add it times both scales while the tensor core fills the next slot.
+//    and the epilogue warps, which hold the tile's fp32 sums in registers, add
+//    it times both scales while the tensor core fills the next slot.  Two
+//    operations of fp32 per value and block take as long as the tensor core's
+//    own work (512 cycles of an SM for 128 x 256 x 128), and the registers
+//    that TMEM values arrive in do not pair up for the two-wide instructions
+//    without a move each: the sums bound large products.
 #include <algorithm>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
-#include "few.cuh"
+#include "weight_stream.cuh"
 
 namespace moe {
 
@@ -43,8 +47,8 @@ __device__ __forceinline__ float lin_act(float z, int relu2) {
 
 struct LinearFewArgs {
     LinearArgs l;
-    FwCut cut;
     FwShare share;
+    int chunks;         // of a weight row
     int slot_bytes, n_stages;
 };
 
@@ -92,7 +96,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
         auto next_unit = [&]() {
             k = w;
             do {
-                if (++unit == a.share.units || k >= a.cut.n) return false;
+                if (++unit == a.share.units || k >= a.chunks) return false;
                 const int u = blockIdx.x * a.share.units + unit;
                 n0 = unit_row(u);
                 n = unit_row(u + 1) - n0;
@@ -101,9 +105,9 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
         };
         const bool active = mine && next_unit();
         auto step = [&]() {
-            put.fill(&maps.w[a.share.rows - n], k * a.cut.chunk, n0, n * a.cut.chunk, policy);
+            put.fill(&maps.w[a.share.rows - n], k * FW_CHUNK, n0, n * FW_CHUNK, policy);
             k += FW_WARPS;
-            return k < a.cut.n || next_unit();
+            return k < a.chunks || next_unit();
         };
         if (!fw_produce(put, active, step, ctx, abort_flag)) fw_settle();
         return;
@@ -113,7 +117,6 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     FwTake ring(rings, warp);
     const int g = lane / 4, q = lane % 4;
     const int M = (int)l.M;
-    using F = FwFmt<false, true, true, true>;
     FwSide<TT> side;
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
@@ -126,16 +129,16 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
         const int n0 = unit_row(u), n = unit_row(u + 1) - n0;
         FwAcc<2, TT> acc;
         acc.clear();
-        if (n > 0 && warp < a.cut.n) {
+        if (n > 0 && warp < a.chunks) {
             side.ws = l.ws + (int64_t)(n0 + min(lane, n - 1)) * l.kb;
-            FwActs<F, fw_batch<F, TT>(), TT> v;
-            fw_fetch(v, side, warp * a.cut.chunk, l.Kp);
-            for (int k = warp; k < a.cut.n;) {
+            FwActs<TT> v;
+            fw_fetch(v, side, warp * FW_CHUNK, l.Kp);
+            for (int k = warp; k < a.chunks;) {
                 if (!ring.wait(ctx, abort_flag)) return fw_settle();
-                fw_mul_stage(acc, ring.data(), n, k * a.cut.chunk, l.Kp, side, v);
+                fw_mul(acc, ring.data(), n, v);
                 ring.release();
                 k += FW_WARPS;
-                if (k < a.cut.n) fw_fetch(v, side, k * a.cut.chunk, l.Kp);
+                if (k < a.chunks) fw_fetch(v, side, k * FW_CHUNK, l.Kp);
             }
         }
         float* mine = red.mine(warp);
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int r = 0; r < 3; ++r)   // rows g + 8 r
-                    mine[(t * 8 + 2 * q + c) * FW_ROWS + g + 8 * r] = acc.sum(r / 2, t, c + 2 * (r % 2));
+                    mine[(t * 8 + 2 * q + c) * FW_ROWS + g + 8 * r] = acc.d[r / 2][t][c + 2 * (r % 2)];
         if (!red.exchange(ctx, abort_flag)) return fw_settle();
         for (int j = tid; j < n * M; j += 32 * FW_WARPS) {
             const int t = j / n, row = j - t * n;
@@ -565,7 +568,7 @@ template <int TT>
 static cudaError_t launch_linear_few(LinearFewArgs& a, int num_sms, const DevCtx& ctx, cudaStream_t stream) {
     LinearFewMaps maps = {};
     for (int i = 0; i < 2 && a.share.rows > i; ++i)
-        if (!fw_map(&maps.w[i], a.l.wq, a.l.N, a.l.Kp, a.l.Kp, a.cut.chunk, a.share.rows - i)) return cudaErrorInvalidValue;
+        if (!fw_map(&maps.w[i], a.l.wq, a.l.N, a.l.Kp, a.l.Kp, FW_CHUNK, a.share.rows - i)) return cudaErrorInvalidValue;
     const size_t fixed = FwRed::bytes(a.share.units) + FwRings::kBarBytes + 8 + 16;
     a.n_stages = (int)std::min<size_t>(FW_MAX_STAGES, (FW_SMEM - fixed) / FW_WARPS / a.slot_bytes);
     const size_t smem = (size_t)FW_WARPS * a.n_stages * a.slot_bytes + fixed;
@@ -599,9 +602,9 @@ static cudaError_t launch_linear(const LinearArgs& l, int num_sms, const DevCtx&
     if (l.M <= kFewMaxTokens) {
         LinearFewArgs a = {};
         a.l = l;
-        a.cut = fw_cut(l.Kp, true);
+        a.chunks = (l.Kp + FW_CHUNK - 1) / FW_CHUNK;
         a.share = fw_share(l.N, num_sms);
-        a.slot_bytes = (a.share.rows * a.cut.chunk + 127) / 128 * 128;
+        a.slot_bytes = (a.share.rows * FW_CHUNK + 127) / 128 * 128;
         return l.M <= 8 ? launch_linear_few<1>(a, num_sms, ctx, stream) : launch_linear_few<2>(a, num_sms, ctx, stream);
     }
     // the widest tile that still gives every SM one
