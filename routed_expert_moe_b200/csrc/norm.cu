@@ -76,7 +76,7 @@ __device__ __forceinline__ float nm_block_sum(float v, float* red, int n_warps) 
 // A block per row at a time (grid-stride); thread i of its n holds the row's 16-byte vectors i + j * n,
 // j < VPT.
 template <int VPT, int MAXT, bool POST, bool CODES>
-__global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 768 / MAXT) norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(MAXT, 1024 / MAXT) norm_kernel(NormArgs a) {
     pdl_enter();
     __shared__ float red[2][2][32];   // [row parity][sum][warp]
     const int nv = a.H / 8;
@@ -211,7 +211,10 @@ static cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t stre
     // Device times, H = 2688 (one vector against three), prenorm to u and postnorm to x', u:
     //   T = 296    2.7 against 3.1 us,   4.3 against  5.7
     //   T = 577    4.3 against 3.5,      7.6 against  6.6
-    //   T = 16384   58 against  32,      153 against   93       (a warp per row: 35, 117)
+    //   T = 16384   58 against  32,      153 against   81       (a warp per row: 35, 117)
+    // What bounds the large ones is how many loads an SM has under way, so 1024 threads fit on it (64
+    // registers each): with 768, postnorm took 93 us.  prenorm to codes (43 us, 21 at the rate of a copy)
+    // is held up by the shuffles of its maxima; warp reductions for them took longer.
     if (a.T >= 3 * num_sms) {
         const int w = (nv + 127) / 128;
         if (w <= 2) return launch_vpt<2, 128>(a, 128, num_sms, stream);
