@@ -164,14 +164,16 @@ constexpr int LT_BM = 128;              // rows of x per tile (TMEM lanes)
 constexpr int LT_KB = 128;              // bytes of K per stage: one scale block
 constexpr int LT_MMA = 2;               // threads that issue products: the issue of one stage takes one thread
                                         // about as long as the tensor core's work for a narrow tile
-constexpr int LT_SC = 8;                // blocks of K of a scale slot
+constexpr int LT_SC = 8;                // blocks of K of a scale slot: whole pairs of stages
 constexpr int LT_SS = 2;                // slots of the scale ring
 constexpr int LT_MAX_STAGES = 8;
 
 template <int BN>
 struct LtShape {
-    static constexpr int kSlots = 4;                  // TMEM partial products
-    static constexpr int kTmem = kSlots * BN;                          // columns
+    // TMEM holds the products of two pairs of stages: taken two at a time, the waits, counters and
+    // branches of a stage's sums cost half as much (they took as many instructions as the sums)
+    static constexpr int kSlots = 2;
+    static constexpr int kTmem = 2 * kSlots * BN;                         // columns
     static constexpr int kStage = (LT_BM + BN) * LT_KB;
     // a scale slot is [LT_SC][kLd] floats; 4 words over a multiple of 32, so that the copies of 4 rows by
     // 8 blocks meet 32 banks
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int p = 0; p < S::kSlots; ++p) {
-            mbar_init(smem_u32(&pfull[p]), 1);
+            mbar_init(smem_u32(&pfull[p]), LT_MMA);
             mbar_init(smem_u32(&pempty[p]), 4 * S::kSets);
         }
         for (int s = 0; s < LT_SS; ++s) {
@@ -389,13 +391,14 @@ __global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
     } else if (warp < 4) {
         if (lane == 0) {
             const uint32_t idesc = make_idesc(0u, LT_BM, BN);
-            const uint32_t m = warp == 3;
+            const int m = warp == 3;
             int stage = 0, ps = 0;
-            uint32_t phase = 0, pph = 0, n = 0;
+            uint32_t phase = 0, pph = 0;
             bool ok = true, issued = false;
             for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                for (int ks = 0; ks < l.kb; ++ks, ++n) {
-                    if (n % LT_MMA == m) {
+                for (int ks = 0; ks < l.kb; ++ks) {
+                    const bool last = ks == l.kb - 1;
+                    if (ks % LT_MMA == m) {
                         if (!mbar_wait(smem_u32(&full[stage]), phase, ctx, abort_flag) ||
                             !mbar_wait(smem_u32(&pempty[ps]), pph ^ 1u, ctx, abort_flag)) {
                             ok = false;
@@ -406,16 +409,23 @@ __global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
                         const uint64_t xd = sw128_desc(xa), wd = sw128_desc(xa + LT_BM * LT_KB);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)   // the block's sum: the slot is overwritten first
-                            mma_ss<true>(tmem_base + ps * BN, xd + 2 * kk, wd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+                            mma_ss<true>(tmem_base + (2 * ps + m) * BN, xd + 2 * kk, wd + 2 * kk, idesc,
+                                         kk != 0 ? 1u : 0u);
                         issued = true;
                         mma_commit(smem_u32(&empty[stage]));
                         mma_commit(smem_u32(&pfull[ps]));
+                    } else if (m == 1 && last) {   // a pair of one: nothing to add to it
+                        if (!mbar_wait(smem_u32(&pempty[ps]), pph ^ 1u, ctx, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive(smem_u32(&pfull[ps]));
                     }
                     if (++stage == NS) {
                         stage = 0;
                         phase ^= 1u;
                     }
-                    if (++ps == S::kSlots) {
+                    if ((ks % 2 == 1 || last) && ++ps == S::kSlots) {
                         ps = 0;
                         pph ^= 1u;
                     }
@@ -447,53 +457,65 @@ __global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
             ok = lt_wait(smem_u32(&sfull[ss]), sph, ctx, abort_flag) && lt_wait(smem_u32(&pfull[ps]), pph, ctx, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            lt_tmem_ld(tq + ps * BN, v[0]);
-            for (int ks = 0, kk = 0; ks < l.kb; ++ks) {
-                const float* sc = reinterpret_cast<const float*>(scales + ss * S::kScale) + kk * S::kLd;
-                uint64_t sx[4];
+            lt_tmem_ld(tq + 2 * ps * BN, v[0]);
+            for (int ks = 0, kk = 0; ks < l.kb; ks += 2) {
+                const bool two = ks + 1 < l.kb;
+                // the sums of one stage, the last of its pair or not
+                auto add = [&](int sub, bool end) {
+                    const float* sc = reinterpret_cast<const float*>(scales + ss * S::kScale) + (kk + sub) * S::kLd;
+                    const uint32_t ta = tq + (2 * ps + sub) * BN;
+                    uint64_t sx[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sx[i] = f2_pack(sc[r0 + 8 * i], sc[r0 + 8 * i]);
-                const float* sw = sc + LT_BM + c0 + 2 * q;
-                const bool chunk_end = ++kk == LT_SC;
+                    for (int i = 0; i < 4; ++i) sx[i] = f2_pack(sc[r0 + 8 * i], sc[r0 + 8 * i]);
+                    const float* sw = sc + LT_BM + c0 + 2 * q;
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    uint64_t w[4];
+                    for (int c = 0; c < NC; ++c) {
+                        uint64_t w[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint64_t*>(sw + c * 32 + j * 8);
+                        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint64_t*>(sw + c * 32 + j * 8);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {   // lanes 0 .. 15, 16 .. 31 of the quadrant
-                        uint32_t(&p)[16] = v[h];
-                        lt_tmem_wait(p);
-                        if (h == 0) lt_tmem_ld(tq + ps * BN + (16u << 16) + c * 32, v[1]);
-                        else if (c + 1 < NC) lt_tmem_ld(tq + ps * BN + (c + 1) * 32, v[0]);
-                        else {   // the last read of the slot: free it, go on to the next
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(smem_u32(&pempty[ps]));
-                            if (++ps == S::kSlots) {
-                                ps = 0;
-                                pph ^= 1u;
+                        for (int h = 0; h < 2; ++h) {   // lanes 0 .. 15, 16 .. 31 of the quadrant
+                            uint32_t(&p)[16] = v[h];
+                            lt_tmem_wait(p);
+                            if (h == 0) lt_tmem_ld(ta + (16u << 16) + c * 32, v[1]);
+                            else if (c + 1 < NC) lt_tmem_ld(ta + (c + 1) * 32, v[0]);
+                            else if (!end) lt_tmem_ld(ta + BN, v[0]);
+                            else {   // the last read of the pair: free it, go on to the next
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(smem_u32(&pempty[ps]));
+                                if (++ps == S::kSlots) {
+                                    ps = 0;
+                                    pph ^= 1u;
+                                }
+                                if (ks + 2 < l.kb) {
+                                    ok = lt_wait(smem_u32(&pfull[ps]), pph, ctx, abort_flag);
+                                    if (!ok) return;
+                                    tc_fence_after();
+                                    lt_tmem_ld(tq + 2 * ps * BN, v[0]);
+                                }
                             }
-                            if (ks + 1 < l.kb) {
-                                ok = lt_wait(smem_u32(&pfull[ps]), pph, ctx, abort_flag);
-                                if (!ok) break;
-                                tc_fence_after();
-                                lt_tmem_ld(tq + ps * BN, v[0]);
-                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const uint64_t pp = f2_pack(__uint_as_float(p[4 * j + 2 * i]),
+                                                                __uint_as_float(p[4 * j + 2 * i + 1]));
+                                    uint64_t& s = acc[2 * h + i][4 * c + j];
+                                    s = f2_fma(f2_mul(pp, w[j]), sx[2 * h + i], s);
+                                }
                         }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint64_t pp =
-                                    f2_pack(__uint_as_float(p[4 * j + 2 * i]), __uint_as_float(p[4 * j + 2 * i + 1]));
-                                uint64_t& s = acc[2 * h + i][4 * c + j];
-                                s = f2_fma(f2_mul(pp, w[j]), sx[2 * h + i], s);
-                            }
                     }
+                };
+                if (two) {
+                    add(0, false);
+                    add(1, true);
+                } else {
+                    add(0, true);
                 }
                 if (!ok) break;
-                if (chunk_end || ks == l.kb - 1) {
+                kk += 2;
+                if (kk == LT_SC || ks + 2 >= l.kb) {
                     kk = 0;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sempty[ss]));
@@ -501,7 +523,7 @@ __global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
                         ss = 0;
                         sph ^= 1u;
                     }
-                    if (ks + 1 < l.kb) {
+                    if (ks + 2 < l.kb) {
                         ok = lt_wait(smem_u32(&sfull[ss]), sph, ctx, abort_flag);
                         if (!ok) break;
                     }
