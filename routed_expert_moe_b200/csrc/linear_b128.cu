@@ -56,7 +56,8 @@ struct LinearFewMaps {
     CUtensorMap w[2];   // boxes of share.rows weight rows, and of one less
 };
 
-template <int TT>
+// MT tiles of 16 weight rows per unit, TT of 8 rows of x.
+template <int MT, int TT>
 __global__ void __launch_bounds__(FW_THREADS, 1)
     linear_few_kernel(const __grid_constant__ LinearFewMaps maps, LinearFewArgs a, DevCtx ctx) {
     extern __shared__ __align__(1024) uint8_t lf_smem[];
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     for (int un = 0; un < a.share.units; ++un) {
         const int u = blockIdx.x * a.share.units + un;
         const int n0 = unit_row(u), n = unit_row(u + 1) - n0;
-        FwAcc<2, TT> acc;
+        FwAcc<MT, TT> acc;
         acc.clear();
         if (n > 0 && warp < a.chunks) {
             side.ws = l.ws + (int64_t)(n0 + min(lane, n - 1)) * l.kb;
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int r = 0; r < 3; ++r)   // rows g + 8 r
+                for (int r = 0; r < MT + 1; ++r)   // rows g + 8 r
                     mine[(t * 8 + 2 * q + c) * FW_ROWS + g + 8 * r] = acc.d[r / 2][t][c + 2 * (r % 2)];
         if (!red.exchange(ctx, abort_flag)) return fw_settle();
         for (int j = tid; j < n * M; j += 32 * FW_WARPS) {
@@ -162,6 +163,8 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
 
 constexpr int LT_BM = 128;              // rows of x per tile (TMEM lanes)
 constexpr int LT_KB = 128;              // bytes of K per stage: one scale block
+constexpr int LT_EPI = 8;               // epilogue warps: two per TMEM lane quadrant
+constexpr int LT_THREADS = 32 * (4 + LT_EPI);
 constexpr int LT_MMA = 2;               // threads that issue products: the issue of one stage takes one thread
                                         // about as long as the tensor core's work for a narrow tile
 constexpr int LT_SC = 8;                // blocks of K of a scale slot: whole pairs of stages
@@ -179,9 +182,7 @@ struct LtShape {
     // 8 blocks meet 32 banks
     static constexpr int kLd = LT_BM + BN + 4;
     static constexpr int kScale = LT_SC * kLd * 4;
-    static constexpr int kSets = BN >= 64 ? 2 : 1;                    // epilogue warps of a TMEM lane quadrant
-    static constexpr int kCols = BN / kSets;                           // columns of an epilogue warp
-    static constexpr int kThreads = 32 * (4 + 4 * kSets);
+    static constexpr int kCols = BN / 2;                               // columns of an epilogue warp
 };
 
 struct LinearTileArgs {
@@ -272,7 +273,7 @@ __device__ __forceinline__ bool lt_wait_long(uint32_t bar, uint32_t parity, cons
 // Persistent over the tiles, the row tiles of one weight tile first.  Warp 0 loads the codes (TMA), warps
 // 1 and 3 issue the products of even and odd stages, warp 2 copies the scales, the others sum and store.
 template <int BN>
-__global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
+__global__ void __launch_bounds__(LT_THREADS, 1)
     linear_tile_kernel(const __grid_constant__ LinearMaps maps, LinearTileArgs a, DevCtx ctx) {
     using S = LtShape<BN>;
     extern __shared__ uint8_t smem_raw[];
@@ -299,11 +300,11 @@ __global__ void __launch_bounds__(LtShape<BN>::kThreads, 1)
         }
         for (int p = 0; p < S::kSlots; ++p) {
             mbar_init(smem_u32(&pfull[p]), LT_MMA);
-            mbar_init(smem_u32(&pempty[p]), 4 * S::kSets);
+            mbar_init(smem_u32(&pempty[p]), LT_EPI);
         }
         for (int s = 0; s < LT_SS; ++s) {
             mbar_init(smem_u32(&sfull[s]), 1);
-            mbar_init(smem_u32(&sempty[s]), 4 * S::kSets);
+            mbar_init(smem_u32(&sempty[s]), LT_EPI);
         }
         for (int m = 0; m < LT_MMA; ++m) mbar_init(smem_u32(drain + m), 1);
         *abort_flag = 0;
@@ -586,7 +587,7 @@ bool fw_map(CUtensorMap* m, const void* base, int64_t rows, int64_t bytes, int64
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int TT>
+template <int MT, int TT>
 static cudaError_t launch_linear_few(LinearFewArgs& a, int num_sms, const DevCtx& ctx, cudaStream_t stream) {
     LinearFewMaps maps = {};
     for (int i = 0; i < 2 && a.share.rows > i; ++i)
@@ -594,7 +595,7 @@ static cudaError_t launch_linear_few(LinearFewArgs& a, int num_sms, const DevCtx
     const size_t fixed = FwRed::bytes(a.share.units) + FwRings::kBarBytes + 8 + 16;
     a.n_stages = (int)std::min<size_t>(FW_MAX_STAGES, (FW_SMEM - fixed) / FW_WARPS / a.slot_bytes);
     const size_t smem = (size_t)FW_WARPS * a.n_stages * a.slot_bytes + fixed;
-    auto k = linear_few_kernel<TT>;
+    auto k = linear_few_kernel<MT, TT>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_k(k, dim3(num_sms), dim3(FW_THREADS), smem, stream, maps, a, ctx);
@@ -617,7 +618,7 @@ static cudaError_t launch_linear_tiles(const LinearArgs& l, int num_sms, const D
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t grid = std::min<int64_t>((int64_t)a.m_tiles * a.n_tiles, num_sms);
-    return launch_k(k, dim3((unsigned)grid), dim3(S::kThreads), smem, stream, maps, a, ctx);
+    return launch_k(k, dim3((unsigned)grid), dim3(LT_THREADS), smem, stream, maps, a, ctx);
 }
 
 static cudaError_t launch_linear(const LinearArgs& l, int num_sms, const DevCtx& ctx, cudaStream_t stream) {
@@ -627,14 +628,22 @@ static cudaError_t launch_linear(const LinearArgs& l, int num_sms, const DevCtx&
         a.chunks = (l.Kp + FW_CHUNK - 1) / FW_CHUNK;
         a.share = fw_share(l.N, num_sms);
         a.slot_bytes = (a.share.rows * FW_CHUNK + 127) / 128 * 128;
-        return l.M <= 8 ? launch_linear_few<1>(a, num_sms, ctx, stream) : launch_linear_few<2>(a, num_sms, ctx, stream);
+        // as many matrix tiles as there are rows for: 1856 weight rows (13 per SM) of 2688 against one row of x
+        // in 3.9 us with one, 4.2 with two; two tiles of x for one of M <= 8 would double the instructions
+        if (a.share.rows <= 16)
+            return l.M <= 8 ? launch_linear_few<1, 1>(a, num_sms, ctx, stream)
+                            : launch_linear_few<1, 2>(a, num_sms, ctx, stream);
+        return l.M <= 8 ? launch_linear_few<2, 1>(a, num_sms, ctx, stream)
+                        : launch_linear_few<2, 2>(a, num_sms, ctx, stream);
     }
-    // the widest tile that still gives every SM one
+    // 64 columns while every tile has an SM of its own, else 128 (us, 64 against 128 columns):
+    //   tiles of 64     42: 64 x 2688 x 1856   8.5, 10.6      84: 256 x 2688 x 1856   8.8, 11.2
+    //                  145: 577 x 1856 x 2688 10.6, 13.7     168: 64 x 10752 x 2688  18.1, 14.3
+    //                  336: 1024 x 2688 x 1856 19.5, 19.1    672: 2048 x 2688 x 1856 30.5, 26.9
+    // (32 columns: 8.9 at 64 x 2688 x 1856, 12.9 at 256.)
     const int64_t mt = (l.M + LT_BM - 1) / LT_BM;
-    auto fills = [&](int bn) { return mt * ((l.N + bn - 1) / bn) >= num_sms; };
-    if (fills(128)) return launch_linear_tiles<128>(l, num_sms, ctx, stream);
-    if (fills(64)) return launch_linear_tiles<64>(l, num_sms, ctx, stream);
-    return launch_linear_tiles<32>(l, num_sms, ctx, stream);
+    if (mt * ((l.N + 63) / 64) <= num_sms) return launch_linear_tiles<64>(l, num_sms, ctx, stream);
+    return launch_linear_tiles<128>(l, num_sms, ctx, stream);
 }
 
 }  // namespace moe
