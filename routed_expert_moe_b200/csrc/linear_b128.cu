@@ -400,7 +400,10 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
                 for (int ks = 0; ks < l.kb; ++ks) {
                     const bool last = ks == l.kb - 1;
                     if (ks % LT_MMA == m) {
-                        if (!mbar_wait(smem_u32(&full[stage]), phase, ctx, abort_flag) ||
+                        // The slot's use before may be the other thread's: until that one is consumed, the parity
+                        // of full may be that of the use two back.
+                        if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, ctx, abort_flag) ||
+                            !mbar_wait(smem_u32(&full[stage]), phase, ctx, abort_flag) ||
                             !mbar_wait(smem_u32(&pempty[ps]), pph ^ 1u, ctx, abort_flag)) {
                             ok = false;
                             break;
