@@ -23,7 +23,7 @@
 // needs another to be resident, and every wait is bounded.
 //
 // Bound: HBM bytes of the touched experts' weights, at one to three tokens the fixed steps around them:
-// two launches, the choice of experts (3 us), a first and a last unit with nothing beside them.  128-row
+// two launches, the choice of experts (3 us), units that are one SM's work alone.  128-row
 // units leave SMs without work at one or two tokens (87 up units at one token of the full sizes), which
 // costs little: a load-only loop of 60 MB takes 16.4 us on 87 SMs and on 148.  Units of 64 rows while
 // there are few were slower (bf16, 3 tokens: 92 against 72 us): a stage of half the weights takes the
@@ -32,9 +32,9 @@
 // H = 2688, E = 128, K = 6, F = 1856, us, against moe_forward, and what the touched weights take at the
 // rate of a copy:
 //   tokens       1                   4                   8                     16
-//   bf16    40 / 53 / 19        88 / 95 / 69       137 / 143 / 129       218 / 215 / 214
-//   E4M3    35 / 41 /  9        51 / 65 / 35        82 /  90 /  64       126 / 127 / 107
-//   B128    37 / 45 / 10        55 / 71 / 36        85 /  96 /  68       130 / 134 / 112
+//   bf16    41 / 53 / 19        90 / 96 / 69       139 / 145 / 129       221 / 219 / 214
+//   E4M3    36 / 42 /  9        52 / 65 / 35        83 /  90 /  64       127 / 128 / 107
+//   B128    37 / 45 / 10        56 / 71 / 36        86 /  96 /  68       133 / 135 / 112
 #include <algorithm>
 #include <climits>
 #include <cstdint>
