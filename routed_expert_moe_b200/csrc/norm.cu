@@ -162,17 +162,27 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) norm_kernel(NormArgs a) {
                 for (int i = 0; i < 8; ++i) f[j][i] *= p[i];
             }
             if (a.u && v < nv) reinterpret_cast<uint4*>(a.u + t * a.H)[v] = nm_pack(f[j]);
-            if constexpr (CODES) {
-                // a block of 128 values is 16 neighbouring lanes (vectors past the row are zero)
-                float m = 0.0f;
+        }
+        if constexpr (CODES) {
+            // a block of 128 values is 16 neighbouring lanes (vectors past the row are zero)
+            float m[VPT];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[j][i]));
+            for (int j = 0; j < VPT; ++j) {
+                m[j] = 0.0f;
 #pragma unroll
-                for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                for (int i = 0; i < 8; ++i) m[j] = fmaxf(m[j], fabsf(f[j][i]));
+            }
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1)
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], off));
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = i0 + j * n;
                 // Not below the smallest normal number, so that 1 / s is finite.  A product with it is
                 // within 2^-23 of the quotient, next to half a step of the codes, 2^-4; a quotient per
                 // value took longer than the bytes.
-                const float s = m > 0.0f ? fmaxf(__fdiv_rn(m, 448.0f), 0x1p-126f) : 1.0f;
+                const float s = m[j] > 0.0f ? fmaxf(__fdiv_rn(m[j], 448.0f), 0x1p-126f) : 1.0f;
                 const float is = __frcp_rn(s);
                 if (v < kb * 16) {
                     uint32_t c[2] = {0, 0};
@@ -213,8 +223,9 @@ static cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t stre
     //   T = 577    4.3 against 3.5,      7.6 against  6.6
     //   T = 16384   58 against  32,      153 against   81       (a warp per row: 35, 117)
     // What bounds the large ones is how many loads an SM has under way, so 1024 threads fit on it (64
-    // registers each): with 768, postnorm took 93 us.  prenorm to codes (43 us, 21 at the rate of a copy)
-    // is held up by the shuffles of its maxima; warp reductions for them took longer.
+    // registers each): with 768, postnorm took 93 us.  prenorm to codes (39 us, 21 at the rate of a copy)
+    // is held up by the shuffles of its maxima, done for all vectors together (one after the other: 43);
+    // warp reductions for them took longer.
     if (a.T >= 3 * num_sms) {
         const int w = (nv + 127) / 128;
         if (w <= 2) return launch_vpt<2, 128>(a, 128, num_sms, stream);
