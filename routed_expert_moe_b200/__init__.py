@@ -231,18 +231,18 @@ def forward_few(d, x, w_router, bias, w_up, w_down, out, ws, scales=None, residu
     sp = ctypes.byref(scales) if scales is not None else None
     su, sd = shared if shared is not None else (None, None)
     where, bf, dev = "moe_forward_few", torch.bfloat16, torch.cuda.current_device()
-    if d.T <= FEW_MAX_TOKENS and d.expert_dtype != MOE_NVFP4:   # else refused below
+    if d.T <= FEW_MAX_TOKENS and d.expert_dtype != MOE_NVFP4:
         wt = bf if d.expert_dtype == MOE_BF16 else torch.uint8
-        kh, kf = (b128_kp(d.H), b128_kp(d.F)) if d.expert_dtype == MOE_FP8_B128 else (d.H, d.F)
-        th, tk = (d.T, d.H), (d.T, d.K)
-        for t, dtype, shape in ((x, bf, th), (w_router, bf, (d.E, d.H)), (bias, torch.float32, (d.E,)),
-                                (w_up, wt, (d.E, d.F, kh)), (w_down, wt, (d.E, d.H, kf)), (su, bf, (d.Fs, d.H)),
-                                (sd, bf, (d.H, d.Fs)), (residual, bf, th), (out, bf, th),
-                                (topk_idx, torch.int32, tk), (topk_w, torch.float32, tk)):
-            _arg(t, where, dtype, shape, dev)
-    _check(_lib.moe_forward_few(ctypes.byref(d), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(w_up), _ptr(w_down),
-                                _ptr(su), _ptr(sd), sp, _ptr(residual), _ptr(out), _ptr(topk_idx), _ptr(topk_w),
-                                _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), where)
+        T, H, E, F = d.T, d.H, d.E, d.F
+        kh, kf = (b128_kp(H), b128_kp(F)) if d.expert_dtype == MOE_FP8_B128 else (H, F)
+        th, tk = (T, H), (T, d.K)
+        p = [_arg(t, where, dtype, shape, dev) for t, dtype, shape in (
+            (x, bf, th), (w_router, bf, (E, H)), (bias, torch.float32, (E,)), (w_up, wt, (E, F, kh)),
+            (w_down, wt, (E, H, kf)), (su, bf, (d.Fs, H)), (sd, bf, (H, d.Fs)), (residual, bf, th), (out, bf, th),
+            (topk_idx, torch.int32, tk), (topk_w, torch.float32, tk))]
+    else:   # refused by the call
+        p = [_ptr(t) for t in (x, w_router, bias, w_up, w_down, su, sd, residual, out, topk_idx, topk_w)]
+    _check(_lib.moe_forward_few(ctypes.byref(d), *p[:7], sp, *p[7:], ws.data_ptr(), ws.nbytes, _stream(stream)), where)
 
 
 def gather_rows(x, perm_src, out, K=1, stream=None):
