@@ -32,9 +32,9 @@
 // H = 2688, E = 128, K = 6, F = 1856, us, against moe_forward, and what the touched weights take at the
 // rate of a copy:
 //   tokens       1                   4                   8                     16
-//   bf16    41 / 53 / 19        90 / 96 / 69       139 / 145 / 129       221 / 219 / 214
+//   bf16    40 / 53 / 19        83 / 96 / 69       139 / 145 / 129       223 / 219 / 214
 //   E4M3    36 / 42 /  9        52 / 65 / 35        83 /  90 /  64       127 / 128 / 107
-//   B128    37 / 45 / 10        56 / 71 / 36        86 /  96 /  68       133 / 135 / 112
+//   B128    37 / 45 / 10        56 / 71 / 36        86 /  97 /  68       131 / 135 / 112
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -620,7 +620,9 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
     } else if (warp == 1 || warp == 7) {
         // ---------------------------------------------------------------- products
         // The issue of a stage's four instructions takes one thread about as long as the stage's share
-        // of HBM: two threads take turns.
+        // of HBM: two threads take turns, one with the even slots of the ring and one with the odd ones.
+        // (By turns within a unit, a slot's uses could be the other thread's, and the parity of full that of the
+        // use two back.)
         if (lane == 0) {
             const int m = warp == 7;
             int stage = 0, qs = 0, slot = 0, other = S::kSlots, u;
@@ -635,11 +637,8 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
                     break;
                 }
                 for (int ks = 0; ks < k_stages; ++ks) {
-                    if (ks % FL_MMA == m) {
-                        // The slot's use before may be the other thread's: until that one is consumed, the parity
-                        // of full may be that of the use two back.
-                        if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, ctx, abort_flag) ||
-                            !mbar_wait(smem_u32(&full[stage]), phase, ctx, abort_flag) ||
+                    if (stage % FL_MMA == m) {
+                        if (!mbar_wait(smem_u32(&full[stage]), phase, ctx, abort_flag) ||
                             (S::BLOCK && !mbar_wait(smem_u32(&rempty[slot]), sph ^ 1u, ctx, abort_flag))) {
                             ok = false;
                             break;
@@ -647,7 +646,7 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
                         tc_fence_after();
                         const uint32_t wa = smem_u32(smem + (size_t)stage * S::kStage);
                         const uint64_t wd = sw128_desc(wa), bd = sw128_desc(wa + FL_A);
-                        const uint32_t d = tmem_base + (uint32_t)((slot * S::kSums + (S::BLOCK ? 0 : 2 * m)) * S::kCols);
+                        const uint32_t d = tmem_base + (uint32_t)((slot * S::kSums + (S::BLOCK ? 0 : 2 * (ks % FL_MMA))) * S::kCols);
                         const uint32_t first = S::BLOCK || ks < FL_MMA ? 0u : 1u;
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)   // 32 bytes of K each (the descriptors count 16)
@@ -833,6 +832,7 @@ static cudaError_t launch_layer(const FewMaps& maps, FewArgs& a, int num_sms, co
     using S = FlShape<FMT>;
     const size_t fixed = 1024 + few_table_bytes(a.n_list_max);
     a.n_stages = (int)std::min<size_t>(FL_MAX_STAGES, (FL_SMEM - fixed) / S::kStage);
+    a.n_stages -= a.n_stages % FL_MMA;   // each slot has one issuer
     const size_t smem = (size_t)a.n_stages * S::kStage + fixed;
     auto k = few_layer_kernel<FMT>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -274,7 +274,9 @@ __device__ __forceinline__ bool lt_wait_long(uint32_t bar, uint32_t parity, cons
 }
 
 // Persistent over the tiles, the row tiles of one weight tile first.  Warp 0 loads the codes (TMA), warps
-// 1 and 3 issue the products of even and odd stages, warp 2 copies the scales, the others sum and store.
+// 1 and 3 issue the products of the ring's even and odd slots (by turns within a tile, a slot's uses could be
+// the other thread's, and the parity of full that of the use two back), warp 2 copies the scales, the others
+// sum and store.
 template <int BN>
 __global__ void __launch_bounds__(LT_THREADS, 1)
     linear_tile_kernel(const __grid_constant__ LinearMaps maps, LinearTileArgs a, DevCtx ctx) {
@@ -402,11 +404,8 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
             for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
                 for (int ks = 0; ks < l.kb; ++ks) {
                     const bool last = ks == l.kb - 1;
-                    if (ks % LT_MMA == m) {
-                        // The slot's use before may be the other thread's: until that one is consumed, the parity
-                        // of full may be that of the use two back.
-                        if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, ctx, abort_flag) ||
-                            !mbar_wait(smem_u32(&full[stage]), phase, ctx, abort_flag) ||
+                    if (stage % LT_MMA == m) {
+                        if (!mbar_wait(smem_u32(&full[stage]), phase, ctx, abort_flag) ||
                             !mbar_wait(smem_u32(&pempty[ps]), pph ^ 1u, ctx, abort_flag)) {
                             ok = false;
                             break;
@@ -416,12 +415,12 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
                         const uint64_t xd = sw128_desc(xa), wd = sw128_desc(xa + LT_BM * LT_KB);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)   // the block's sum: the slot is overwritten first
-                            mma_ss<true>(tmem_base + (2 * ps + m) * BN, xd + 2 * kk, wd + 2 * kk, idesc,
+                            mma_ss<true>(tmem_base + (2 * ps + ks % 2) * BN, xd + 2 * kk, wd + 2 * kk, idesc,
                                          kk != 0 ? 1u : 0u);
                         issued = true;
                         mma_commit(smem_u32(&empty[stage]));
                         mma_commit(smem_u32(&pfull[ps]));
-                    } else if (m == 1 && last) {   // a pair of one: nothing to add to it
+                    } else if (last && ks % 2 == 0) {   // a pair of one: nothing to add to it
                         if (!mbar_wait(smem_u32(&pempty[ps]), pph ^ 1u, ctx, abort_flag)) {
                             ok = false;
                             break;
@@ -619,6 +618,7 @@ static cudaError_t launch_linear_tiles(const LinearArgs& l, int num_sms, const D
     a.n_tiles = (l.N + BN - 1) / BN;
     const size_t fixed = 1024 + LT_SS * S::kScale + (2 * LT_MAX_STAGES + 2 * S::kSlots + 2 * LT_SS + LT_MMA) * 8 + 16;
     a.n_stages = (int)std::min<size_t>(LT_MAX_STAGES, (FW_SMEM - fixed) / S::kStage);
+    a.n_stages -= a.n_stages % LT_MMA;   // each slot has one issuer
     const size_t smem = (size_t)a.n_stages * S::kStage + fixed;
     auto k = linear_tile_kernel<BN>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
