@@ -49,6 +49,7 @@ struct DeviceInfo {
 };
 
 constexpr int kMaxDevices = 64;
+constexpr int kMaxSmemKernels = 64;   // kernels that take more than 48 KB of shared memory (38 now)
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 
@@ -399,6 +400,29 @@ moe_status check_fp8_scales(const moe_dims* d, const moe_fp8_scales* sc) {
 namespace moe {
 bool pdl_enabled() { return g_pdl.load() != 0; }
 bool shared_map_2d() { return g_shared_2d.load() != 0; }
+
+cudaError_t allow_smem_once(const void* kernel, int bytes) {
+    struct Entry {
+        const void* kernel;
+        uint64_t devices;   // a bit per device whose limit is written
+    };
+    static Entry known[kMaxSmemKernels];
+    static int n = 0;
+    static std::mutex mu;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    int i = 0;
+    while (i < n && known[i].kernel != kernel) ++i;
+    if (i == kMaxSmemKernels) return cudaErrorInvalidDeviceFunction;
+    if (i == n) known[n++] = {kernel, 0};
+    if ((known[i].devices >> dev) & 1u) return cudaSuccess;
+    const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (set == cudaSuccess) known[i].devices |= (uint64_t)1 << dev;
+    return set;
+}
 // Device context and argument checks for entry points defined in other files.
 moe_status internal_check_dims(const moe_dims* d) { return check_dims(d); }
 moe_status internal_device(DevCtx* ctx, int* num_sms) {

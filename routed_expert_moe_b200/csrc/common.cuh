@@ -284,6 +284,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// Shared memory a block may have.
+constexpr int kMaxSmem = 227 * 1024;
+
+// Host: lets blocks of `kernel` have `bytes` of dynamic shared memory, a constant of the kernel.  The limit is
+// the function's, for every host thread of the process: one of the call's own size could be lowered by another
+// thread's call before this one's launch.  It is written once per kernel and device.
+cudaError_t allow_smem_once(const void* kernel, int bytes);
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kernel)(KArgs...), int bytes = kMaxSmem) {
+    return allow_smem_once(reinterpret_cast<const void*>(kernel), bytes);
+}
+
 // Host: launch `kernel` on `stream`, marked for programmatic stream
 // serialization unless that is switched off (moe_debug_set what = 6).
 bool pdl_enabled();

@@ -191,7 +191,6 @@ constexpr int FL_N = 16;            // token columns
 constexpr int FL_B = FL_N * FL_KB;
 constexpr int FL_UQ = 4;            // unit queue slots
 constexpr int FL_MAX_STAGES = 12;
-constexpr int FL_SMEM = 227 * 1024;
 // Bytes of each shared matrix that are fetched into L2 while the routing is found.
 constexpr int64_t kFewWarmBytes = (int64_t)24 << 20;
 static_assert(kFewMaxTokens == FL_N, "a token per column");
@@ -831,11 +830,11 @@ template <int FMT>
 static cudaError_t launch_layer(const FewMaps& maps, FewArgs& a, int num_sms, const DevCtx& ctx, cudaStream_t stream) {
     using S = FlShape<FMT>;
     const size_t fixed = 1024 + few_table_bytes(a.n_list_max);
-    a.n_stages = (int)std::min<size_t>(FL_MAX_STAGES, (FL_SMEM - fixed) / S::kStage);
+    a.n_stages = (int)std::min<size_t>(FL_MAX_STAGES, (kMaxSmem - fixed) / S::kStage);
     a.n_stages -= a.n_stages % FL_MMA;   // each slot has one issuer
     const size_t smem = (size_t)a.n_stages * S::kStage + fixed;
     auto k = few_layer_kernel<FMT>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(k);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)a.n_list_max * (a.m_up + a.m_down);
     return launch_k(k, dim3((unsigned)std::min<int64_t>(units, num_sms)), dim3(FL_THREADS), smem, stream, maps, a, ctx);

@@ -542,7 +542,7 @@ cudaError_t launch_grouped_ffn(bool fp8, const void* w_up, const void* w_down, i
     const size_t smem = 1024 + (size_t)ns * stage_bytes + (size_t)(2 * ns + 5) * 8 + 16 + 16 +
                         (size_t)FF_EPI_WARPS * 16 * 32 * sizeof(uint16_t) + 2 * FF_UQ * sizeof(uint64_t) +
                         FF_UQ * sizeof(int);
-    cudaError_t err = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t err = allow_smem(kfn);
     if (err != cudaSuccess) return err;
     return launch_k(kfn, dim3(grid), dim3(FF_THREADS), smem, stream, maps, g, ctx);
 }

@@ -394,7 +394,7 @@ template <bool FP8, bool UP, bool SHD = false>
 static cudaError_t launch_one(const GemmMaps& maps, const GemmArgs& g, int grid, size_t smem, const DevCtx& ctx,
                               cudaStream_t stream) {
     auto kfn = grouped_gemm_kernel<FP8, UP, SHD>;
-    cudaError_t err = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t err = allow_smem(kfn);
     if (err != cudaSuccess) return err;
     return launch_k(kfn, dim3(grid), dim3(GG_THREADS), smem, stream, maps, g, ctx);
 }

@@ -381,7 +381,7 @@ template <bool FP8, bool UP>
 static cudaError_t launch_pair(const Gemm2Maps& maps, const Gemm2Args& g, int64_t max_units, int num_sms, size_t smem,
                         const DevCtx& ctx, cudaStream_t stream) {
     auto kfn = grouped_gemm_pair_kernel<FP8, UP>;
-    cudaError_t err = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t err = allow_smem(kfn);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];

@@ -680,7 +680,7 @@ cudaError_t launch_grouped_gemm_b128(bool up, const uint8_t* W, const float* w_s
     const int grid = (int)(max_units < num_sms ? max_units : num_sms);
     auto kfn = bn > 64 ? (up ? grouped_gemm_b128_kernel<true, 128> : grouped_gemm_b128_kernel<false, 128>)
                        : (up ? grouped_gemm_b128_kernel<true, 64> : grouped_gemm_b128_kernel<false, 64>);
-    cudaError_t err = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t err = allow_smem(kfn);
     if (err != cudaSuccess) return err;
     return launch_k(kfn, dim3(grid), dim3(GB_THREADS), smem, stream, maps, g, ctx);
 }
@@ -737,7 +737,7 @@ cudaError_t launch_grouped_ffn_b128(const uint8_t* w_up, const float* su, const 
     const int64_t slots = (int64_t)num_sms * 2;   // two CTAs per SM
     const int grid = (int)(max_units < slots ? max_units : slots);
     auto kfn = grouped_ffn_b128_kernel<FB_BN>;
-    cudaError_t err = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t err = allow_smem(kfn);
     if (err != cudaSuccess) return err;
     return launch_k(kfn, dim3(grid), dim3(GB_THREADS), smem, stream, maps, g, ctx);
 }

@@ -598,10 +598,10 @@ static cudaError_t launch_linear_few(LinearFewArgs& a, int num_sms, const DevCtx
     for (int i = 0; i < 2 && a.share.rows > i; ++i)
         if (!fw_map(&maps.w[i], a.l.wq, a.l.N, a.l.Kp, a.l.Kp, FW_CHUNK, a.share.rows - i)) return cudaErrorInvalidValue;
     const size_t fixed = FwRed::bytes(a.share.units) + FwRings::kBarBytes + 8 + 16;
-    a.n_stages = (int)std::min<size_t>(FW_MAX_STAGES, (FW_SMEM - fixed) / FW_WARPS / a.slot_bytes);
+    a.n_stages = (int)std::min<size_t>(FW_MAX_STAGES, (kMaxSmem - fixed) / FW_WARPS / a.slot_bytes);
     const size_t smem = (size_t)FW_WARPS * a.n_stages * a.slot_bytes + fixed;
     auto k = linear_few_kernel<MT, TT>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(k);
     if (e != cudaSuccess) return e;
     return launch_k(k, dim3(num_sms), dim3(FW_THREADS), smem, stream, maps, a, ctx);
 }
@@ -617,11 +617,11 @@ static cudaError_t launch_linear_tiles(const LinearArgs& l, int num_sms, const D
     a.m_tiles = (int)((l.M + LT_BM - 1) / LT_BM);
     a.n_tiles = (l.N + BN - 1) / BN;
     const size_t fixed = 1024 + LT_SS * S::kScale + (2 * LT_MAX_STAGES + 2 * S::kSlots + 2 * LT_SS + LT_MMA) * 8 + 16;
-    a.n_stages = (int)std::min<size_t>(LT_MAX_STAGES, (FW_SMEM - fixed) / S::kStage);
+    a.n_stages = (int)std::min<size_t>(LT_MAX_STAGES, (kMaxSmem - fixed) / S::kStage);
     a.n_stages -= a.n_stages % LT_MMA;   // each slot has one issuer
     const size_t smem = (size_t)a.n_stages * S::kStage + fixed;
     auto k = linear_tile_kernel<BN>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(k);
     if (e != cudaSuccess) return e;
     const int64_t grid = std::min<int64_t>((int64_t)a.m_tiles * a.n_tiles, num_sms);
     return launch_k(k, dim3((unsigned)grid), dim3(LT_THREADS), smem, stream, maps, a, ctx);

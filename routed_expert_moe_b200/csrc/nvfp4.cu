@@ -1067,7 +1067,7 @@ template <bool UP, bool SMALL>
 static cudaError_t launch_fp4(const Fp4Maps& maps, const Fp4Args& g, int grid, size_t smem, cudaStream_t stream,
                               const DevCtx& ctx) {
     auto kfn = grouped_gemm_fp4_kernel<UP, SMALL>;
-    cudaError_t err = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t err = allow_smem(kfn);
     if (err != cudaSuccess) return err;
     return launch_k(kfn, dim3(grid), dim3(FG_THREADS), smem, stream, maps, g, ctx);
 }
@@ -1157,7 +1157,7 @@ cudaError_t launch_grouped_ffn_fp4(const uint8_t* wu_codes, const uint8_t* wu_sc
     const int64_t slots = (int64_t)num_sms * (small ? Fp4Tmem<true>::CTAS : Fp4Tmem<false>::CTAS);
     const int grid = (int)(max_units < slots ? max_units : slots);
     auto kfn = small ? grouped_ffn_fp4_kernel<true> : grouped_ffn_fp4_kernel<false>;
-    cudaError_t err = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t err = allow_smem(kfn);
     if (err != cudaSuccess) return err;
     return launch_k(kfn, dim3(grid), dim3(FG_THREADS), smem, stream, maps, g, ctx);
 }

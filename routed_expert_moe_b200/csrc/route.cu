@@ -934,7 +934,7 @@ static int64_t fused_max_clusters(int num_sms) {
     using L = RfLayout<NTH, CS>;
     auto kfn = router_fused_kernel<NTH, CS>;
     int n = 0;
-    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes) == cudaSuccess) {
+    if (allow_smem(kfn) == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -967,7 +967,7 @@ template <int NTH, int CS>
 static cudaError_t launch_router_fused(const RouterFusedArgs& ra, const DevCtx& ctx, cudaStream_t stream) {
     using L = RfLayout<NTH, CS>;
     auto kfn = router_fused_kernel<NTH, CS>;
-    cudaError_t err = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes);
+    cudaError_t err = allow_smem(kfn);
     if (err != cudaSuccess) return err;
     const unsigned tiles = (unsigned)((ra.T + L::BT - 1) / L::BT);
     return launch_k(kfn, dim3(tiles * CS), dim3(NTH), L::bytes, stream, ra, ctx);
@@ -988,7 +988,7 @@ static int router_small_max_clusters(int TB, int H, int E) {
     cfg.gridDim = dim3(RS_CLUSTER);
     cfg.blockDim = dim3(RS_THREADS);
     cfg.dynamicSmemBytes = smem;
-    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+    if (allow_smem(kfn, (int)kRouterSmallSmemMax) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kfn, &cfg) != cudaSuccess || n < 1) {
         (void)cudaGetLastError();
         n = 1;
@@ -1017,7 +1017,7 @@ template <int TB>
 static cudaError_t launch_router_small(const RouterSmallArgs& ra, const DevCtx& ctx, cudaStream_t stream) {
     const size_t smem = rs_smem_bytes(TB, ra.H, ra.E);
     auto kfn = router_small_kernel<TB>;
-    cudaError_t err = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t err = allow_smem(kfn, (int)kRouterSmallSmemMax);
     if (err != cudaSuccess) return err;
     const unsigned groups = (unsigned)((ra.T + TB - 1) / TB);
     // clusters that only warm L2: those the device still fits beside the batch's groups

@@ -549,7 +549,7 @@ cudaError_t launch_route_tc(const uint16_t* x, const uint16_t* wr, const float* 
     const int64_t tiles = (T + RC_NT - 1) / RC_NT;
     RouterMmaArgs ma{T, E, (H + RC_KB - 1) / RC_KB, splits, part};
     const size_t smem = 1024 + (size_t)RC_STAGES * RC_STAGE_BYTES + 2 * RC_STAGES * 8 + 16 + 16;
-    err = cudaFuncSetAttribute(router_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    err = allow_smem(router_mma_kernel);
     if (err != cudaSuccess) return err;
     err = launch_k(router_mma_kernel, dim3((unsigned)(tiles * splits)), dim3(RC_THREADS), smem, stream, maps, ma, ctx);
     if (err != cudaSuccess) return err;

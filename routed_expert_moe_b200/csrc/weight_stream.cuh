@@ -45,7 +45,6 @@ constexpr int FW_THREADS = 32 * (FW_WARPS + FW_PROD);
 constexpr int FW_SEG = 64;                    // bytes of a row that one matrix step takes
 constexpr int FW_ROWS = 24;                   // weight rows per stage at most
 constexpr int FW_MAX_STAGES = 6;              // of one warp's ring
-constexpr int FW_SMEM = 227 * 1024;           // shared memory a block may use
 
 constexpr int FW_SEGS = 6;                    // segments per stage: whole blocks of 128, one scale each
 constexpr int FW_CHUNK = FW_SEGS * FW_SEG;    // bytes of a row per stage
