@@ -56,6 +56,14 @@ std::mutex g_dev_mu;
 moe_status device_setup(DeviceInfo** out) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MOE_ECUDA;
+    // A host thread has no context current before its first runtime call that needs one, and the driver
+    // refuses to encode tensor maps without.  This one changes nothing and may run during a graph capture.
+    static thread_local int t_current = -1;
+    if (t_current != dev) {
+        int least, greatest;
+        if (cudaDeviceGetStreamPriorityRange(&least, &greatest) != cudaSuccess) return MOE_ECUDA;
+        t_current = dev;
+    }
     std::lock_guard<std::mutex> lock(g_dev_mu);
     DeviceInfo& d = g_dev[dev];
     if (!d.ready) {

@@ -55,6 +55,33 @@ CALLS = {
 }
 
 
+@pytest.mark.parametrize("make", [lambda moe: layer(moe, 3, True), lambda moe: layer(moe, 3, True, "b128"),
+                                  lambda moe: product(moe, 3, 144), lambda moe: product(moe, 40, 144),
+                                  lambda moe: layer(moe, 3, False)],
+                         ids=["few", "few_b128", "product_few", "product", "forward"])
+def test_the_first_call_of_a_host_thread(moe, make):
+    """A new thread has no CUDA context current before its first runtime call."""
+    call, out = make(moe)
+    call(None)
+    torch.cuda.synchronize()
+    want, stream, refused = out.clone(), torch.cuda.current_stream(), []
+    out.zero_()
+    torch.cuda.synchronize()
+
+    def work():
+        try:
+            call(stream)
+        except moe.MoeError as e:
+            refused.append(str(e))
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not refused, refused
+    assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("what,threads,rounds", [(w, 8, 20000) if w == "few" else (w, 4, 8000) for w in CALLS],
                          ids=list(CALLS))
 def test_host_threads_do_not_disturb_one_another(moe, what, threads, rounds):
