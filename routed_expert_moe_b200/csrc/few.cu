@@ -800,6 +800,7 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
                     last = atomicAdd(summed + blk * 4 + q, 1) == n_list - 1;
                     __threadfence();
                 }
+                __syncwarp();   // the other lanes read too, and the shuffle orders no memory
                 if (__shfl_sync(0xffffffffu, last, 0))
                     fl_combine(a, sel_w, blk * FL_BM + q * 32 + lane % 8 * 4, lane / 8);
                 __syncwarp();
