@@ -367,25 +367,43 @@ __global__ void __launch_bounds__(LT_THREADS, 1)
             const int64_t m0 = (t % a.m_tiles) * LT_BM;
             const int n0 = (int)(t / a.m_tiles) * BN;
             for (int ks = 0; ks < l.kb; ks += LT_SC) {
-                if (!__all_sync(0xffffffffu, lt_wait_long(smem_u32(&sempty[ss]), sph ^ 1u, ctx, abort_flag))) {
-                    ok = false;
-                    break;
-                }
                 const bool in_k = ks + kk < l.kb;
                 float* sd = reinterpret_cast<float*>(scales + ss * S::kScale) + kk * S::kLd + r0;
                 const float* xs = l.xs + (m0 + r0) * l.kb + ks + kk;
                 const float* ws = l.ws + (int64_t)(n0 + r0) * l.kb + ks + kk;
                 const int step = 4 * l.kb, mx = in_k ? (int)min((int64_t)LT_BM, l.M - m0) : 0;
                 const int mw = in_k ? min(BN, l.N - n0) : 0;
-                float vx[LT_BM / 4], vw[BN / 4];   // all in flight
+                if (!__all_sync(0xffffffffu, lt_wait_long(smem_u32(&sempty[ss]), sph ^ 1u, ctx, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                // A tile of 64 columns has an SM for itself and little to wait for: all reads under way at once.
+                // Else 16 (4096 x 10752 x 2688: 206 us; with 8 of them 210, and with all of a slot's 208, in the
+                // way of the sums' reads of shared memory).
+                if constexpr (BN == 64) {
+                    float vx[LT_BM / 4], vw[BN / 4];
 #pragma unroll
-                for (int i = 0; i < LT_BM / 4; ++i) vx[i] = r0 + 4 * i < mx ? __ldg(xs + i * step) : 0.0f;
+                    for (int i = 0; i < LT_BM / 4; ++i) vx[i] = r0 + 4 * i < mx ? xs[i * step] : 0.0f;
 #pragma unroll
-                for (int i = 0; i < BN / 4; ++i) vw[i] = r0 + 4 * i < mw ? __ldg(ws + i * step) : 0.0f;
+                    for (int i = 0; i < BN / 4; ++i) vw[i] = r0 + 4 * i < mw ? ws[i * step] : 0.0f;
 #pragma unroll
-                for (int i = 0; i < LT_BM / 4; ++i) sd[4 * i] = vx[i];
+                    for (int i = 0; i < LT_BM / 4; ++i) sd[4 * i] = vx[i];
 #pragma unroll
-                for (int i = 0; i < BN / 4; ++i) sd[LT_BM + 4 * i] = vw[i];
+                    for (int i = 0; i < BN / 4; ++i) sd[LT_BM + 4 * i] = vw[i];
+                } else {
+                    static_assert(LT_BM % 64 == 0 && BN % 64 == 0, "whole copies");
+                    auto copy = [&](float* to, const float* from, int rows) {   // 64 rows
+                        float v[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = r0 + 4 * i < rows ? from[i * step] : 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) to[4 * i] = v[i];
+                    };
+#pragma unroll
+                    for (int r = 0; r < LT_BM; r += 64) copy(sd + r, xs + r / 4 * step, mx - r);
+#pragma unroll
+                    for (int r = 0; r < BN; r += 64) copy(sd + LT_BM + r, ws + r / 4 * step, mw - r);
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sfull[ss]));
                 if (++ss == LT_SS) {

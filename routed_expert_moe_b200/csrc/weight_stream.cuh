@@ -243,8 +243,8 @@ __device__ __forceinline__ void fw_fetch(FwActs<NT>& v, const FwSide<NT>& side, 
 #pragma unroll
     for (int b = 0; b < FwActs<NT>::KB; ++b) {
         const bool in = full || c0 + b * 128 < row_bytes;
-        v.ws[b] = in ? __ldg(side.ws + c0 / 128 + b) : 0.0f;
-        v.xs[b] = in ? __ldg(side.xs + c0 / 128 + b) : 0.0f;
+        v.ws[b] = in ? side.ws[c0 / 128 + b] : 0.0f;
+        v.xs[b] = in ? side.xs[c0 / 128 + b] : 0.0f;
     }
 }
 
