@@ -132,7 +132,9 @@ const char* moe_status_string(moe_status s);
 int moe_abi_version(void);
 
 /* Bytes of workspace that moe_forward needs for these dims (moe_route,
- * moe_permute and moe_expert_ffn need no more).  Host only; no device call. */
+ * moe_permute, moe_expert_ffn and moe_forward_few need no more).  Never less for
+ * more tokens: a workspace for the largest batch serves every smaller one.
+ * Host only; no device call. */
 moe_status moe_workspace_size(const moe_dims* d, size_t* bytes);
 
 /* Number of kernels one moe_forward call with these dims launches on its

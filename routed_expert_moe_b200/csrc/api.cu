@@ -468,7 +468,10 @@ moe_status moe_workspace_size(const moe_dims* d, size_t* bytes) {
     // plans depend on the SM count only through the router split; size for
     // the largest split any device can choose
     *bytes = forward_ws_bytes(d, 1024);
-    if (few_supported(d)) *bytes = std::max(*bytes, few_ws_bytes(d));
+    // a workspace for more tokens than the few-token layer takes serves its batches too
+    moe_dims few = *d;
+    few.T = std::min<int64_t>(d->T, kFewMaxTokens);
+    if (few_supported(&few)) *bytes = std::max(*bytes, few_ws_bytes(&few));
     return MOE_OK;
 }
 
