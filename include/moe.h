@@ -222,8 +222,9 @@ moe_status moe_forward(const moe_dims* d, const void* x, const void* w_router, c
  *    h_scale (correctly rounded) before the code.  A token's bits do not depend on
  *    which other tokens share its batch.
  *  - ws_bytes is moe_workspace_size(d)'s, as for moe_forward.
- *  - out may alias residual, but not x.  Calls that may overlap on the GPU need
- *    workspaces of their own, as with moe_forward. */
+ *  - out may be residual itself, but neither overlap it otherwise nor overlap x
+ *    (MOE_EINVAL).  Calls that may overlap on the GPU need workspaces of their
+ *    own, as with moe_forward. */
 moe_status moe_forward_few(const moe_dims* d, const void* x, const void* w_router, const float* bias,
                            const void* w_up, const void* w_down, const void* w_up_shared,
                            const void* w_down_shared, const moe_fp8_scales* scales, const void* residual,
@@ -325,8 +326,9 @@ moe_status moe_rmsnorm(int64_t T, int32_t H, float eps, const void* x, void* u, 
  * All sums and v in fp32 (the codes come from v before its rounding to bf16).
  *   x, u [T][H] bf16; gain [H] bf16 or NULL (1); codes [T][Kp(H)], scales [T][Kp(H)/128]
  *   fp32, Kp(H) = 128*ceil(H/128): both given or both NULL; u may be NULL when codes are given.
- * u may alias x.  16 <= H <= 65536, a multiple of 16; T < 2^31.  Cited: audio.cpp
- * model page, "Q4_K, Q3_K and Q2_K expert profiles" (the model's normalisation);
+ * u may be x itself; outputs that overlap one another or an input otherwise are
+ * refused.  16 <= H <= 65536, a multiple of 16; T < 2^31.  Cited: audio.cpp model
+ * page, "Q4_K, Q3_K and Q2_K expert profiles" (the model's normalisation);
  * bloomery page s.3 (FP8_B128). */
 moe_status moe_prenorm(int64_t T, int32_t H, float eps, const void* x, const void* gain, void* u, uint8_t* codes,
                        float* scales, void* stream);
@@ -338,8 +340,9 @@ moe_status moe_prenorm(int64_t T, int32_t H, float eps, const void* x, const voi
  *   u, codes, scales: moe_prenorm of x' (fp32, before its rounding) with next_gain and eps;
  *   all three NULL: x_out only.
  *   y, x, x_out [T][H] bf16; gain, next_gain [H] bf16 or NULL (1); gate bf16 or NULL (1):
- *   [H] with gate_ld 0, or [T][H] with gate_ld H.  x_out may alias x or y, u may alias y;
- *   x_out and u are different.  Sizes as in moe_prenorm. */
+ *   [H] with gate_ld 0, or [T][H] with gate_ld H.  x_out and u may each be x, y or a gate
+ *   per token itself; outputs that overlap one another or an input otherwise are refused.
+ *   Sizes as in moe_prenorm. */
 moe_status moe_postnorm(int64_t T, int32_t H, float eps, float alpha, const void* y, const void* gain,
                         const void* gate, int64_t gate_ld, const void* x, void* x_out, const void* next_gain,
                         void* u, uint8_t* codes, float* scales, void* stream);
@@ -349,7 +352,7 @@ moe_status moe_postnorm(int64_t T, int32_t H, float eps, float alpha, const void
  *   z[m][n] = sum_b x_scales[m][b] * w_scales[n][b] * sum_{k in block b} x[m][k] * w[n][k]
  *   out[m][n] = bf16(z) (MOE_ACT_NONE) or bf16(relu(z)^2) (MOE_ACT_RELU2), summed in fp32.
  *   x_codes [M][Kp(K)], x_scales [M][Kp(K)/128], w_codes [N][Kp(K)], w_scales
- *   [N][Kp(K)/128], out [M][N] bf16; codes past K zero in both operands.
+ *   [N][Kp(K)/128], out [M][N] bf16, which may overlap none of them; codes past K zero in both operands.
  * 0 <= M < 2^31 - 128; 16 <= N <= 2^20, 16 <= K <= 65536, both multiples of 16.  No workspace.
  * Cited: bloomery page s.3 ("Kernel dispatch": FP8_B128), s.2 (ReLU^2). */
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU2 = 1 } moe_act;

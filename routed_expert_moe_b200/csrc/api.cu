@@ -636,7 +636,8 @@ moe_status moe_forward_few(const moe_dims* d, const void* x, const void* w_route
         !aligned(residual, 16) || !aligned(out, 16) || !aligned(ws, 256) || !aligned(bias, 4) ||
         !aligned(topk_idx, 4) || !aligned(topk_w, 4))
         return MOE_EINVAL;
-    if (d->T > 0 && out == x) return MOE_EINVAL;
+    const int64_t act = d->T * (int64_t)d->H * 2;
+    if (overlap(out, act, x, act) || shifted(out, residual, act)) return MOE_EINVAL;
     if (d->T == 0) return MOE_OK;
     DeviceInfo* dev = nullptr;
     if ((s = device_setup(&dev)) != MOE_OK) return s;

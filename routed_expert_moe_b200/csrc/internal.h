@@ -113,6 +113,14 @@ cudaError_t launch_quantize(int64_t n_tensors, int64_t elems, const uint16_t* sr
 cudaError_t launch_ep_regroup(const int64_t* recv_counts, int W, int E_loc, int64_t R, int32_t* offsets,
                               int32_t* perm, int32_t* inv, const DevCtx& ctx, cudaStream_t stream);
 
+// Buffers of an entry point's caller: whether two share a byte, and whether they do without being the same
+// (a row may be written in place, but not over a neighbour that is still to be read).  Null: no.
+inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return p && q && p < q + (uintptr_t)nb && q < p + (uintptr_t)na;
+}
+inline bool shifted(const void* a, const void* b, int64_t n) { return a != b && overlap(a, n, b, n); }
+
 // The few-token layer (few.cu): at most this many tokens, the columns of its matrix instructions.
 constexpr int kFewMaxTokens = 16;
 struct FewWs {

@@ -686,6 +686,10 @@ moe_status moe_linear_fp8_b128(int64_t M, int32_t N, int32_t K, const uint8_t* x
     auto al = [](const void* p, uintptr_t n) { return p && reinterpret_cast<uintptr_t>(p) % n == 0; };
     if (!al(x_codes, 16) || !al(w_codes, 16) || !al(out, 16) || !al(x_scales, 4) || !al(w_scales, 4))
         return MOE_EINVAL;
+    const int64_t kb = (K + 127) / 128, out_bytes = M * N * 2;
+    if (overlap(out, out_bytes, x_codes, M * kb * 128) || overlap(out, out_bytes, x_scales, M * kb * 4) ||
+        overlap(out, out_bytes, w_codes, N * kb * 128) || overlap(out, out_bytes, w_scales, N * kb * 4))
+        return MOE_EINVAL;
     DevCtx ctx;
     int sms = 0;
     const moe_status s = internal_device(&ctx, &sms);

@@ -264,6 +264,27 @@ moe_status check_norm(int64_t T, int32_t H, float eps) {
 bool codes_ok(const uint8_t* codes, const float* scales) {
     return !codes == !scales && is_aligned(codes, 16) && is_aligned(scales, 4);
 }
+
+// A row of bf16 outputs may replace the row of inputs that it is made of; nothing else may be shared.
+bool buffers_ok(const NormArgs& a) {
+    const int64_t row = (int64_t)a.H * 2, act = a.T * row, kb = (a.H + 127) / 128;
+    const bool per_token = a.gate_ld != 0;
+    const struct {
+        const void* p;
+        int64_t n;
+        bool rows;   // [T][H] bf16
+    } out[4] = {{a.x_out, act, true}, {a.u, act, true}, {a.codes, a.T * kb * 128, false}, {a.scales, a.T * kb * 4, false}},
+      in[5] = {{a.x, act, true}, {a.y, act, true}, {a.gate, per_token ? act : row, per_token},
+               {a.gain_post, row, false}, {a.gain_pre, row, false}};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 5; ++j)
+            if (!(out[i].rows && in[j].rows && out[i].p == in[j].p) && overlap(out[i].p, out[i].n, in[j].p, in[j].n))
+                return false;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return false;
+    }
+    return true;
+}
 }  // namespace
 
 extern "C" {
@@ -284,6 +305,7 @@ moe_status moe_prenorm(int64_t T, int32_t H, float eps, const void* x, const voi
     a.T = T;
     a.H = H;
     a.eps = eps;
+    if (!buffers_ok(a)) return MOE_EINVAL;
     return run_norm(a, stream);
 }
 
@@ -295,7 +317,7 @@ moe_status moe_postnorm(int64_t T, int32_t H, float eps, float alpha, const void
     if (!(alpha > -3.4e38f && alpha < 3.4e38f)) return MOE_EINVAL;
     if (gate && gate_ld != 0 && gate_ld != H) return MOE_EINVAL;
     if (T == 0) return MOE_OK;
-    if (!y || !x || !x_out || x_out == u || !codes_ok(codes, scales)) return MOE_EINVAL;
+    if (!y || !x || !x_out || !codes_ok(codes, scales)) return MOE_EINVAL;
     if (!is_aligned(y, 16) || !is_aligned(gain, 16) || !is_aligned(gate, 16) || !is_aligned(x, 16) ||
         !is_aligned(x_out, 16) || !is_aligned(next_gain, 16) || !is_aligned(u, 16))
         return MOE_EINVAL;
@@ -314,6 +336,7 @@ moe_status moe_postnorm(int64_t T, int32_t H, float eps, float alpha, const void
     a.H = H;
     a.eps = eps;
     a.alpha = alpha;
+    if (!buffers_ok(a)) return MOE_EINVAL;
     return run_norm(a, stream);
 }
 
