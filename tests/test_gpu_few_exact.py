@@ -1,4 +1,4 @@
-"""The few-token layer bit for bit, on layers whose sums are exact."""
+"""The few-token layer bit for bit, on layers whose sums are exact; and tokens that are equal."""
 import pytest
 import torch
 
@@ -53,3 +53,12 @@ def test_every_bit(moe, fmt, T, H, E, K, F, ns):
     want = X.output(s)[0].bfloat16()
     wrong = out.cpu() != want
     assert not bool(wrong.any()), (int(wrong.sum()), wrong.nonzero()[:4].tolist())
+
+
+@pytest.mark.parametrize("fmt", X.FORMATS)
+def test_equal_tokens_get_equal_outputs(moe, fmt):
+    s = X.make(16, 400, 32, 4, 304, fmt, seed=5)
+    s["x"][:] = s["x"][3]
+    out, idx, _ = run(moe, s, residual=False)
+    assert torch.equal(out, out[:1].expand_as(out)) and torch.equal(idx, idx[:1].expand_as(idx))
+    assert float(out.abs().max()) > 0
