@@ -144,13 +144,17 @@ def alloc_workspace(d: MoeDims, device=None):
 
 
 def fp8_scales(w_up_scale, w_down_scale, x_scale: float, h_scale: float) -> MoeFp8Scales:
-    return MoeFp8Scales(w_up_scale.data_ptr(), w_down_scale.data_ptr(), float(x_scale), float(h_scale), None, None)
+    sc = MoeFp8Scales(w_up_scale.data_ptr(), w_down_scale.data_ptr(), float(x_scale), float(h_scale), None, None)
+    sc.tensors = (w_up_scale, w_down_scale)   # what the pointers point to lives as long as they do
+    return sc
 
 
 def nvfp4_scales(w_up_tscale, w_down_tscale, x_scale: float, h_scale: float, w_up_block, w_down_block) -> MoeFp8Scales:
     """Tensor scales [E] (fp32), static activation tensor scales, block-scale banks (uint8)."""
-    return MoeFp8Scales(w_up_tscale.data_ptr(), w_down_tscale.data_ptr(), float(x_scale), float(h_scale),
-                        w_up_block.data_ptr(), w_down_block.data_ptr())
+    sc = MoeFp8Scales(w_up_tscale.data_ptr(), w_down_tscale.data_ptr(), float(x_scale), float(h_scale),
+                      w_up_block.data_ptr(), w_down_block.data_ptr())
+    sc.tensors = (w_up_tscale, w_down_tscale, w_up_block, w_down_block)
+    return sc
 
 
 def nvfp4_scale_row(K: int) -> int:
