@@ -244,6 +244,15 @@ def forward_few(d, x, w_router, bias, w_up, w_down, out, ws, scales=None, residu
             (x, bf, th), (w_router, bf, (E, H)), (bias, torch.float32, (E,)), (w_up, wt, (E, F, kh)),
             (w_down, wt, (E, H, kf)), (su, bf, (d.Fs, H)), (sd, bf, (H, d.Fs)), (residual, bf, th), (out, bf, th),
             (topk_idx, torch.int32, tk), (topk_w, torch.float32, tk))]
+        if wt is not bf and hasattr(scales, "tensors"):
+            n = (E, E) if d.expert_dtype == MOE_FP8_E4M3 else (E * F * (kh // 128), E * H * (kf // 128))
+            for t, values in zip(scales.tensors, n):
+                if t.numel() != values:
+                    raise MoeError(MOE_EINVAL, f"{where}: needs {values} scales of a bank, got {tuple(t.shape)}")
+                _arg(t, where, torch.float32, t.shape, dev)
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise MoeError(MOE_EINVAL, f"{where}: needs a contiguous workspace on the current CUDA device, got one on "
+                                       f"{ws.device}")
     else:   # refused by the call
         p = [_ptr(t) for t in (x, w_router, bias, w_up, w_down, su, sd, residual, out, topk_idx, topk_w)]
     _check(_lib.moe_forward_few(ctypes.byref(d), *p[:7], sp, *p[7:], ws.data_ptr(), ws.nbytes, _stream(stream)), where)
