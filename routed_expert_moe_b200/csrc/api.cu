@@ -395,6 +395,7 @@ moe_status check_shared(const moe_dims* d, const void* w_up_s, const void* w_dow
 moe_status check_fp8_scales(const moe_dims* d, const moe_fp8_scales* sc) {
     if (d->expert_dtype == MOE_BF16) return MOE_OK;
     if (!sc || !sc->w_up_scale || !sc->w_down_scale) return MOE_EINVAL;
+    if (!aligned(sc->w_up_scale, 4) || !aligned(sc->w_down_scale, 4)) return MOE_EINVAL;
     if (!(sc->x_scale > 0.0f) || !(sc->h_scale > 0.0f)) return MOE_EINVAL;
     if (!(sc->x_scale < 3.4e38f) || !(sc->h_scale < 3.4e38f)) return MOE_EINVAL;
     if (d->expert_dtype == MOE_NVFP4 && (!sc->w_up_block || !sc->w_down_block || !aligned(sc->w_up_block, 16) ||
