@@ -27,6 +27,8 @@
  *    Errors found inside kernels (an out-of-range expert index, a bounded
  *    wait that expired, a router magnitude outside the exact range) are
  *    recorded in a per-device error word that moe_check_device_error reads.
+ *  - Any host thread may call, several at once.  Calls that may overlap on the
+ *    GPU need outputs and workspaces of their own.
  *  - Results are deterministic: the same inputs give the same bits, on any
  *    stream, at any batch size split (no floating-point atomics).
  *  - Expert indices and the permutation are exact: the router ranks experts
@@ -212,7 +214,7 @@ moe_status moe_forward(const moe_dims* d, const void* x, const void* w_router, c
  * layer, arguments and workspace as moe_forward, for the decode steps of a few
  * requests, where moe_forward's launches and its tiles of 64 token rows cost
  * more than the few expert rows they serve.  Up to 11 tokens it is the faster of
- * the two in every format; at 16 the two are within 2 % of one another.
+ * the two in every format; at 16 the two are within 3 % of one another.
  *  - expert_dtype MOE_BF16 (with or without a shared expert), MOE_FP8_E4M3 or
  *    MOE_FP8_B128; T > 16 and MOE_NVFP4 return MOE_EUNSUPPORTED.
  *  - Indices are those of moe_route bit for bit, weights within fp32 rounding.

@@ -49,7 +49,7 @@ struct DeviceInfo {
 };
 
 constexpr int kMaxDevices = 64;
-constexpr int kMaxSmemKernels = 64;   // kernels that take more than 48 KB of shared memory (38 now)
+constexpr int kMaxSmemKernels = 64;   // kernels that take more than 48 KB of shared memory (42 now)
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 

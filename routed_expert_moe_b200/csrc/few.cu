@@ -25,12 +25,12 @@
 // Bound: HBM bytes of the touched experts' weights, at one to three tokens the fixed steps around them:
 // two launches, the choice of experts (3 us), units that are one SM's work alone.  128-row
 // units leave SMs without work at one or two tokens (87 up units at one token of the full sizes), which
-// costs little: a load-only loop of 60 MB takes 16.4 us on 87 SMs and on 148.  Units of 64 rows while
-// there are few were slower (bf16, 3 tokens: 92 against 72 us): a stage of half the weights takes the
-// same products.
+// costs little: a load-only kernel takes 12.3 us for those 60 MB (bf16) and 8.2 for 30 MB (E4M3), launch
+// included, on 74, 87, 126 and 148 SMs alike.  Units of 64 rows while there are few were slower (bf16, 3
+// tokens: 92 against 72 us): a stage of half the weights takes the same products.
 //
 // H = 2688, E = 128, K = 6, F = 1856, us, against moe_forward, and what the touched weights take at the
-// rate of a copy:
+// rate of a copy (experts chosen nearly evenly: 68 of 128 by 16 tokens):
 //   tokens       1                   4                   8                     16
 //   bf16    40 / 53 / 19        83 / 96 / 69       139 / 145 / 129       223 / 219 / 214
 //   E4M3    36 / 42 /  9        52 / 65 / 35        83 /  90 /  64       127 / 128 / 107
@@ -619,7 +619,8 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
     } else if (warp == 1 || warp == 7) {
         // ---------------------------------------------------------------- products
         // The issue of a stage's four instructions takes one thread about as long as the stage's share
-        // of HBM: two threads take turns, one with the even slots of the ring and one with the odd ones.
+        // of HBM (330 cycles, in a branch of one lane as here; from a converged warp it was not measured):
+        // two threads take turns, one with the even slots of the ring and one with the odd ones.
         // (By turns within a unit, a slot's uses could be the other thread's, and the parity of full that of the
         // use two back.)
         if (lane == 0) {

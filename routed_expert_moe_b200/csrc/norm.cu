@@ -226,6 +226,10 @@ static cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t stre
     // registers each): with 768, postnorm took 93 us.  prenorm to codes (39 us, 21 at the rate of a copy)
     // is held up by the shuffles of its maxima, done for all vectors together (one after the other: 43);
     // warp reductions for them took longer.
+    // The price of 64 registers: postnorm spills 40 to 80 bytes a thread in the forms of four vectors (8 in
+    // that of three with codes) and 460 to 630 in that of eight, which prenorm spills from as well (52, with
+    // codes 284).  Three vectors exist for 128 threads alone, the class of H = 2688: just above 4096 and 8192
+    // values a little more than half of the vector slots hold data.
     if (a.T >= 3 * num_sms) {
         const int w = (nv + 127) / 128;
         if (w <= 2) return launch_vpt<2, 128>(a, 128, num_sms, stream);

@@ -4,14 +4,15 @@
 // A weight row is read once from HBM and meets at most 16 activation rows, so
 // the work is a stream.  Each of a CTA's eight consumer warps has a ring in
 // shared memory of its own.  A lane of one of four producer warps fills it
-// (one TMA box, 16 to 24 rows of a chunk of K, per stage; with one producer
+// (one TMA box, up to 24 rows of a chunk of K, per stage; with one producer
 // warp the issue of the boxes bounds the stream).  A consumer fetches the
 // activations that go with its next stage into registers, waits for the
 // weights, multiplies with warp-level matrix instructions (weights as the
 // 16-row operand, tokens as the 8-column one) and hands the slot back.  No
 // consumer waits for another within a stream.  tcgen05 would need 128 weight
-// rows per instruction, 15 units for 1856 rows; boxes of 16 to 24 rows let
-// every SM stream the same number of bytes.
+// rows per instruction, 15 units for 1856 rows; boxes of as many rows as an SM's
+// share (13 of 1856; several units of at most 24 beyond that) let every SM
+// stream the same number of bytes.
 //
 // Copying row by row instead (untiled bulk copies) costs a fixed 32 cycles of
 // an SM's copy engine per row: 4.6 TB/s at 512 bytes per row, against 7.0 with
@@ -46,7 +47,13 @@ constexpr int FW_SEG = 64;                    // bytes of a row that one matrix 
 constexpr int FW_ROWS = 24;                   // weight rows per stage at most
 constexpr int FW_MAX_STAGES = 6;              // of one warp's ring
 
-constexpr int FW_SEGS = 6;                    // segments per stage: whole blocks of 128, one scale each
+// Segments per stage: whole blocks of 128, one scale each.  Six, chunks of 384 bytes, are seven chunks of a
+// row of 2688 and five of 1920, one for each warp at most; where they are nine or more, some warps work twice
+// while others wait, and eight segments are a little faster (us, for 4 / 6 / 8 segments; M x N x K):
+//   1 x 1856 x 2688  4.1 / 3.9 / 4.0     16 x 1856 x 2688  4.7 / 4.5 / 4.7     8 x 10752 x 2688  14.3 / 12.4 / 13.0
+//   1 x 2688 x 1920  4.0 / 4.0 / 4.2      1 x 1856 x 3200  4.3 / 4.4 / 4.2      8 x 5376 x 3200   8.5 /  8.9 /  8.3
+//   1 x 1856 x 4096  4.6 / 4.8 / 4.4
+constexpr int FW_SEGS = 6;
 constexpr int FW_CHUNK = FW_SEGS * FW_SEG;    // bytes of a row per stage
 
 // Registers: a block of 12 warps starts with 168 per thread.  The consumers' operands need more, the
