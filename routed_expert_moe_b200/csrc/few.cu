@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
     } else if (warp == 1 || warp == 7) {
         // ---------------------------------------------------------------- products
         // The issue of a stage's four instructions takes one thread about as long as the stage's share
-        // of HBM (330 cycles, in a branch of one lane as here; from a converged warp it was not measured):
+        // of HBM (320 to 400 cycles, in a branch of one lane as here; from a converged warp it was not measured):
         // two threads take turns, one with the even slots of the ring and one with the odd ones.
         // (By turns within a unit, a slot's uses could be the other thread's, and the parity of full that of the
         // use two back.)

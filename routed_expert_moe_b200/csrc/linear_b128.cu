@@ -166,7 +166,7 @@ constexpr int LT_KB = 128;              // bytes of K per stage: one scale block
 constexpr int LT_EPI = 8;               // epilogue warps: two per TMEM lane quadrant
 constexpr int LT_THREADS = 32 * (4 + LT_EPI);
 constexpr int LT_MMA = 2;               // threads that issue products: the issue of one stage takes one thread
-                                        // about as long as the tensor core's work for a narrow tile (475 cycles,
+                                        // about as long as the tensor core's work for a narrow tile (410 to 480 cycles,
                                         // in a branch of one lane; from a converged warp it was not measured)
 constexpr int LT_SC = 8;                // blocks of K of a scale slot: whole pairs of stages
 constexpr int LT_SS = 2;                // slots of the scale ring
