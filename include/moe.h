@@ -325,7 +325,8 @@ moe_status moe_rmsnorm(int64_t T, int32_t H, float eps, const void* x, void* u, 
  *                  all-zero block)
  *   codes[t][h] = e4m3(fl32(v[t][h] * fl32(1 / scales[t][h / 128]))), nearest-even, saturating;
  *                 zero past H
- * All sums and v in fp32 (the codes come from v before its rounding to bf16).
+ * All sums and v in fp32 (the codes come from v before its rounding to bf16): a row whose sum of
+ * squares leaves fp32's range (values from about 2^58 on at H = 2688) gives zeros, not the quotient.
  *   x, u [T][H] bf16; gain [H] bf16 or NULL (1); codes [T][Kp(H)], scales [T][Kp(H)/128]
  *   fp32, Kp(H) = 128*ceil(H/128): both given or both NULL; u may be NULL when codes are given.
  * u may be x itself; outputs that overlap one another or an input otherwise are
