@@ -24,9 +24,9 @@ namespace moe {
 constexpr int CB_THREADS = 256;
 
 template <int KMAX>
-__global__ void __launch_bounds__(CB_THREADS) combine_kernel(const uint16_t* __restrict__ yp,
-                                                             const int32_t* __restrict__ inv_row,
-                                                             const float* __restrict__ w,
+__global__ void __launch_bounds__(CB_THREADS) combine_kernel(const uint16_t* yp,
+                                                             const int32_t* inv_row,
+                                                             const float* w,
                                                              const uint16_t* residual, uint16_t* out,
                                                              int64_t T, int K, int ns, int H,
                                                              int64_t rows, DevCtx ctx) {
@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(CB_THREADS) combine_kernel(const uint16_t* __r
 // u = bf16(x / sqrt(mean(x^2) + eps)): sum of squares in fixed point (each
 // x^2, exact in fp32, rounded to 2^-16 and summed exactly in int64), the rest
 // in correctly rounded fp32, so the result is bit-reproducible anywhere.
-__global__ void __launch_bounds__(256) rmsnorm_kernel(const uint16_t* __restrict__ x,
-                                                      uint16_t* __restrict__ u, int64_t T, int H,
+__global__ void __launch_bounds__(256) rmsnorm_kernel(const uint16_t* x,
+                                                      uint16_t* u, int64_t T, int H,
                                                       float eps) {
     pdl_enter();
     const int lane = threadIdx.x % 32;
@@ -149,25 +149,33 @@ __global__ void __launch_bounds__(256) rmsnorm_kernel(const uint16_t* __restrict
         ms = __fadd_rn(ms, eps);
         const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(ms));
         uint4* ur = reinterpret_cast<uint4*>(u + t * H);
-        for (int v = lane; v < nv; v += 32) {
-            const uint4 q = xr[v];
-            const uint32_t qq[4] = {q.x, q.y, q.z, q.w};
-            uint32_t o[4];
+        constexpr int B = 4;   // reads under way before their stores (4096 rows: 10.8 us, one by one 13.2)
+        for (int v0 = lane; v0 < nv; v0 += 32 * B) {
+            uint4 q[B];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float a = __fmul_rn(__uint_as_float(qq[j] << 16), rstd);
-                const float b = __fmul_rn(__uint_as_float(qq[j] & 0xFFFF0000u), rstd);
-                o[j] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(a)) |
-                       ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(b)) << 16);
+            for (int b = 0; b < B; ++b)
+                if (v0 + 32 * b < nv) q[b] = xr[v0 + 32 * b];
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                if (v0 + 32 * b >= nv) break;
+                const uint32_t qq[4] = {q[b].x, q[b].y, q[b].z, q[b].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float lo = __fmul_rn(__uint_as_float(qq[j] << 16), rstd);
+                    const float hi = __fmul_rn(__uint_as_float(qq[j] & 0xFFFF0000u), rstd);
+                    o[j] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(lo)) |
+                           ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(hi)) << 16);
+                }
+                ur[v0 + 32 * b] = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            ur[v] = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
 
 // amax over each tensor (as the bits of |v|, which order like the values).
-__global__ void __launch_bounds__(256) amax_kernel(const uint16_t* __restrict__ src, int64_t elems,
-                                                   unsigned int* __restrict__ amax_bits) {
+__global__ void __launch_bounds__(256) amax_kernel(const uint16_t* src, int64_t elems,
+                                                   unsigned int* amax_bits) {
     pdl_enter();
     const int64_t tensor = blockIdx.y;
     const uint16_t* p = src + tensor * elems;
@@ -192,9 +200,9 @@ __global__ void finalize_scale_kernel(float* scales, int64_t n) {
     }
 }
 
-__global__ void __launch_bounds__(256) quantize_kernel(const uint16_t* __restrict__ src, int64_t elems,
-                                                       const float* __restrict__ scales,
-                                                       uint8_t* __restrict__ codes) {
+__global__ void __launch_bounds__(256) quantize_kernel(const uint16_t* src, int64_t elems,
+                                                       const float* scales,
+                                                       uint8_t* codes) {
     pdl_enter();
     const int64_t tensor = blockIdx.y;
     const float s = scales[tensor];

@@ -117,8 +117,9 @@ __device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity, u
 // thread, before it reads or writes memory that another kernel touches, so
 // a kernel never completes before its predecessor.  Outside a programmatic
 // launch both instructions return at once.  What a preceding kernel may have
-// written is read by ordinary loads: a read-only load (ld.global.nc, __ldg)
-// wants memory that does not change while this kernel exists, and this kernel
+// written is read by ordinary loads: a read-only load (ld.global.nc, __ldg,
+// or one the compiler chooses for a const pointer that is restrict) wants
+// memory that does not change while this kernel exists, and this kernel
 // exists before its predecessor ends.
 __device__ __forceinline__ void pdl_enter() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

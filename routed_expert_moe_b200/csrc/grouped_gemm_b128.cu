@@ -575,8 +575,8 @@ __global__ void __launch_bounds__(GB_THREADS, 2)
 
 // One warp per (row, block of 128): scale amax / 448 (1 for a zero block),
 // codes e4m3(fl32(w / scale)) nearest-even and saturating, zero past K.
-__global__ void quantize_fp8_b128_kernel(const uint16_t* __restrict__ src, int64_t rows, int K, int Kp,
-                                         uint8_t* __restrict__ codes, float* __restrict__ scales) {
+__global__ void quantize_fp8_b128_kernel(const uint16_t* src, int64_t rows, int K, int Kp,
+                                         uint8_t* codes, float* scales) {
     const int nb = Kp / 128;
     const int lane = threadIdx.x % 32;
     const int64_t warps = (int64_t)gridDim.x * (blockDim.x / 32);

@@ -93,8 +93,8 @@ __device__ __forceinline__ void bf16x16(const uint4& a, const uint4& b, float (&
 
 // ----------------------------------------------------------------------------- quantisers
 
-__global__ void __launch_bounds__(256) nvfp4_amax_kernel(const uint16_t* __restrict__ src, int64_t elems,
-                                                         unsigned int* __restrict__ amax_bits) {
+__global__ void __launch_bounds__(256) nvfp4_amax_kernel(const uint16_t* src, int64_t elems,
+                                                         unsigned int* amax_bits) {
     pdl_enter();
     const uint16_t* p = src + (int64_t)blockIdx.y * elems;
     uint32_t m = 0;
@@ -115,9 +115,9 @@ __global__ void nvfp4_tensor_scale_kernel(float* scales, int64_t n) {
 }
 
 // One thread per (tensor, row, block slot of the padded scale row).
-__global__ void __launch_bounds__(256) nvfp4_quantize_kernel(const uint16_t* __restrict__ src, int64_t n_tensors,
-                                                             int64_t rows, int K, const float* __restrict__ tscale,
-                                                             uint8_t* __restrict__ codes, uint8_t* __restrict__ bscale) {
+__global__ void __launch_bounds__(256) nvfp4_quantize_kernel(const uint16_t* src, int64_t n_tensors,
+                                                             int64_t rows, int K, const float* tscale,
+                                                             uint8_t* codes, uint8_t* bscale) {
     pdl_enter();
     const int nb = K / 16, ksp = (nb + 15) / 16 * 16;
     const int64_t total = n_tensors * rows * ksp;
@@ -140,10 +140,10 @@ __global__ void __launch_bounds__(256) nvfp4_quantize_kernel(const uint16_t* __r
 
 // Activation rows: out row r = x[perm_src[r] / K] (or row r when perm_src is null),
 // quantised with the static tensor scale s_t.  One warp per row, a lane per block.
-__global__ void __launch_bounds__(256) nvfp4_gather_kernel(const uint16_t* __restrict__ x,
-                                                           const int32_t* __restrict__ perm_src, int64_t rows,
+__global__ void __launch_bounds__(256) nvfp4_gather_kernel(const uint16_t* x,
+                                                           const int32_t* perm_src, int64_t rows,
                                                            int K, int64_t T, int H, float s_t,
-                                                           uint8_t* __restrict__ codes, uint8_t* __restrict__ bscale,
+                                                           uint8_t* codes, uint8_t* bscale,
                                                            int* zero, int64_t n_zero, DevCtx ctx) {
     pdl_enter();
     // counters of the kernel that follows (the one-launch NVFP4 FFN), zero before it starts

@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(NT) permute_kernel(PermuteArgs a, DevCtx ctx) 
 // assignments per block; the stable rank inside a chunk is computed exactly
 // as in the single-block kernel, and chunks are ordered by their index.
 
-__global__ void __launch_bounds__(PM_THREADS) perm_hist_kernel(const int32_t* __restrict__ idx, int64_t n, int E,
-                                                               int* __restrict__ bcount, DevCtx ctx) {
+__global__ void __launch_bounds__(PM_THREADS) perm_hist_kernel(const int32_t* idx, int64_t n, int E,
+                                                               int* bcount, DevCtx ctx) {
     pdl_enter();
     __shared__ int hist[256];
     const int tid = threadIdx.x;
@@ -206,8 +206,8 @@ __global__ void __launch_bounds__(PM_THREADS) perm_hist_kernel(const int32_t* __
 }
 
 // counts, offsets, per-(chunk, expert) bases, and the GEMM schedule
-__global__ void __launch_bounds__(256) perm_scan_kernel(const int* __restrict__ bcount, int G, int E,
-                                                        int* __restrict__ bbase, int32_t* counts,
+__global__ void __launch_bounds__(256) perm_scan_kernel(const int* bcount, int G, int E,
+                                                        int* bbase, int32_t* counts,
                                                         int32_t* offsets, int4* sched, int* n_sched, int bn,
                                                         int ns, int Tsh, int row0) {
     pdl_enter();
@@ -237,10 +237,10 @@ __global__ void __launch_bounds__(256) perm_scan_kernel(const int* __restrict__ 
     if (sched) build_schedule(offs, E, bn, nb, sched, n_sched, ns, Tsh, row0);
 }
 
-__global__ void __launch_bounds__(PM_THREADS) perm_scatter_kernel(const int32_t* __restrict__ idx, int64_t n,
-                                                                  int E, const int* __restrict__ bbase,
-                                                                  int32_t* __restrict__ perm_src,
-                                                                  int32_t* __restrict__ inv_row) {
+__global__ void __launch_bounds__(PM_THREADS) perm_scatter_kernel(const int32_t* idx, int64_t n,
+                                                                  int E, const int* bbase,
+                                                                  int32_t* perm_src,
+                                                                  int32_t* inv_row) {
     pdl_enter();
     extern __shared__ int wtab[];   // [32][E]
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -298,9 +298,9 @@ __device__ __forceinline__ float div_by_scale(float x, float s, float y) {
 // with perm_src == null the rows are taken in order (xp[r] = x[r]).  Rows
 // r >= routed_rows are the shared expert's: xp[r] = x[(r - routed_rows) % T].  One
 // warp per row, four 16-byte loads per lane in flight before their stores.
-__global__ void gather_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ perm_src,
+__global__ void gather_rows_kernel(const uint16_t* x, const int32_t* perm_src,
                                    int64_t rows, int64_t routed_rows, int K, int64_t T, int H,
-                                   void* __restrict__ xp, int fp8, float x_scale, int* zero, int64_t n_zero,
+                                   void* xp, int fp8, float x_scale, int* zero, int64_t n_zero,
                                    DevCtx ctx) {
     pdl_enter();
     // counters of the kernel that follows (the one-launch FFN), zero before it starts
@@ -423,9 +423,9 @@ cudaError_t launch_gather(const uint16_t* x, const int32_t* perm_src, int64_t ro
 constexpr int RG_THREADS = 512;
 constexpr int RG_MAX_ENTRIES = 256;
 
-__global__ void __launch_bounds__(RG_THREADS) ep_regroup_kernel(const int64_t* __restrict__ rc, int W, int E_loc,
-                                                                int64_t R, int32_t* __restrict__ offsets,
-                                                                int32_t* __restrict__ perm, int32_t* __restrict__ inv,
+__global__ void __launch_bounds__(RG_THREADS) ep_regroup_kernel(const int64_t* rc, int W, int E_loc,
+                                                                int64_t R, int32_t* offsets,
+                                                                int32_t* perm, int32_t* inv,
                                                                 DevCtx ctx) {
     pdl_enter();
     __shared__ int64_t src_base[RG_MAX_ENTRIES + 1];               // [W + 1]
